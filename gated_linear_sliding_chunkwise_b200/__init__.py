@@ -6,4 +6,4 @@ this package does not load the library; importing ``.lizard`` does, and fails
 loudly when it is missing.
 """
 
-__all__ = ["lizard", "synth"]
+__all__ = ["lizard", "paged", "synth"]

@@ -1012,6 +1012,8 @@ lizard_status lizard_workspace_status(void *workspace, lizard_stream_t stream) {
   if (word != 0 && cudaMemset(workspace, 0, sizeof(word)) != cudaSuccess) return LIZARD_ERR_CUDA;
   if (word & 1u) return LIZARD_ERR_TIMEOUT;
   if (word & 2u) return LIZARD_ERR_RANGE;
+  if (word & 4u) return LIZARD_ERR_INDEX;
+  if (word & 8u) return LIZARD_ERR_PAGES;
   return LIZARD_OK;
 }
 
@@ -1024,6 +1026,8 @@ const char *lizard_status_string(lizard_status s) {
     case LIZARD_ERR_TIMEOUT: return "a kernel gave up on a bounded wait";
     case LIZARD_ERR_WORKSPACE: return "workspace missing or too small";
     case LIZARD_ERR_RANGE: return "gate decay outside the tensor-core forward's range (use the portable kernels)";
+    case LIZARD_ERR_INDEX: return "paged cache: a page, row, length, offset or duplicate is not allowed";
+    case LIZARD_ERR_PAGES: return "paged cache: too few free pages";
   }
   return "unknown status";
 }

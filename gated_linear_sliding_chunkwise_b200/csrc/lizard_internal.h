@@ -299,4 +299,61 @@ cudaError_t tc_gla_bwd_preload();
 cudaError_t launch_tc_finish(const FinishBwdArgs &a, int BH, cudaStream_t s);
 cudaError_t launch_finish_bwd(const FinishBwdArgs &a, int BH, int D, bool bf16, cudaStream_t s);
 
+
+// ------------------------------------------------------ paged cache -------
+namespace paged {
+struct Split;
+constexpr int kSMs = 148;                       // SMs of a B200
+// CTAs that share a class's work: portable and streaming kernels two per SM,
+// the tile kernel one.
+constexpr int kSimtCtas = 2 * kSMs, kStreamCtas = 2 * kSMs, kTileCtas = kSMs;
+constexpr int kStreamRows = 16, kTileRows2 = 256, kSimtRows = 64;   // rows of an item
+constexpr int kMaxGroup = 64;                   // query heads per key/value head
+}  // namespace paged
+
+struct PagedArgs {
+  const void *q, *k, *v;
+  void *k_pages, *v_pages;       // this layer's
+  const int *table, *lens, *cu_q, *row;
+  void *o;
+  float *lse;
+  int num_pages, Hkv, page, d, rows, max_pages, B, T, H, g, max_q, window, sinks;
+  float scale;
+  uint32_t *status;
+  paged::Split *split;           // [2]
+  long long *prefix;             // [2][B + 1]
+  // partial sums per class: [slots][rows][d] fp32 and [slots][rows] (maximum, sum)
+  float *part_o[2];
+  float *part_ml[2];
+};
+// Checks the batch, writes the split of its work (tiles per sequence of each
+// class; `few` = class 0 takes sequences of at most kStreamRows rows) and puts
+// k, v into their pages.
+struct PagedGeometry {
+  int few;                       // rows up to which a sequence belongs to class 0
+  int kt[2], tok[2], ctas[2];    // keys per tile, tokens per item, CTAs of each class
+  int least[2];                  // fewest tiles a CTA takes
+};
+cudaError_t launch_paged_prep(const PagedArgs &a, const PagedGeometry &g, bool bf16, cudaStream_t s);
+cudaError_t launch_paged_simt(const PagedArgs &a, const PagedGeometry &g, bool bf16, cudaStream_t s);
+// Joins the pieces of split items (`slot_rows` rows per partial slot).
+cudaError_t launch_paged_join(const PagedArgs &a, const PagedGeometry &g, int cls, int slot_rows, bool bf16,
+                              cudaStream_t s);
+
+struct PagesArgs {
+  int layers, num_pages, page, rows, max_pages, n;
+  size_t page_bytes;             // of one page in one layer (all heads), K or V
+  void *k_pages, *v_pages;
+  int *refs, *table, *lens;
+  const int *row, *src, *grow;
+  int *table_out, *refs_out;
+  uint32_t *status;              // workspace regions from here
+  int *count;                    // [32]: counts of the cluster's CTAs, copies to make
+  int *mark, *need, *offset, *held, *list, *from, *to, *snap;
+};
+cudaError_t launch_pages_reserve(const PagesArgs &a, cudaStream_t s);
+cudaError_t launch_pages_free(const PagesArgs &a, cudaStream_t s);
+cudaError_t launch_pages_fork(const PagesArgs &a, cudaStream_t s);
+cudaError_t launch_pages_compact(const PagesArgs &a, cudaStream_t s);
+
 }  // namespace lz

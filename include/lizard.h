@@ -79,7 +79,9 @@ typedef enum {
   LIZARD_ERR_CUDA = 3,        /* a launch or CUDA runtime call failed */
   LIZARD_ERR_TIMEOUT = 4,     /* a kernel gave up on a bounded wait */
   LIZARD_ERR_WORKSPACE = 5,   /* workspace NULL or smaller than the queried size */
-  LIZARD_ERR_RANGE = 6        /* tensor-core backward: more wide-decay sequences than its exact fallback takes */
+  LIZARD_ERR_RANGE = 6,       /* tensor-core backward: more wide-decay sequences than its exact fallback takes */
+  LIZARD_ERR_INDEX = 7,       /* paged cache: a page, row, length, offset or duplicate found on the device is not allowed */
+  LIZARD_ERR_PAGES = 8        /* paged cache: too few free pages */
 } lizard_status;
 
 typedef enum { LIZARD_BF16 = 0, LIZARD_FP32 = 1 } lizard_dtype;
@@ -412,6 +414,136 @@ typedef struct {
 lizard_status lizard_prefill_cache(const lizard_cache_args *args, lizard_stream_t stream);
 
 /*
+ * Paged key/value cache: the growing cache of a model's softmax layers (the
+ * 50 % hybrid of the Chinese summary, section 2.2, keeps half of them), cut
+ * into pages of a fixed number of tokens so that sequences of any lengths
+ * share one pool.  It stands beside the fixed-size cache of
+ * lizard_decode_step, which serves the other layers.
+ *
+ * The cache is the caller's arrays:
+ *   k_pages, v_pages  [layers, num_pages, Hkv, page, d] dtype; page p holds
+ *                     the same tokens in every layer
+ *   table             [rows, max_pages] int32: row r's token t lies in page
+ *                     table[r][t / page], slot t mod page; -1 = no page
+ *   lens              [rows] int32: tokens of each row
+ *   refs              [num_pages] int32: how many rows hold a page; a page
+ *                     with count 0 is free
+ * Sizes: page in {16, 32, 64, 128}; d in {64, 128}; num_pages <= 2^22;
+ * num_pages * Hkv * page < 2^31; rows * max_pages < 2^31 (addresses are
+ * 64-bit throughout).
+ *
+ * lizard_paged_attn: attention of new tokens over one layer's pages.  The
+ * batch is ragged: sequence b's new tokens are rows cu_q[b] .. cu_q[b+1] - 1
+ * of q, and they are the last ones of the lens[row] tokens of its table row
+ * (one token when decoding, a chunk of a prompt otherwise, any mixture):
+ *   n_b = cu_q[b+1] - cu_q[b],  token i at position p = lens[row] - n_b + i
+ *   with k and v given, they are first written into their pages
+ *   token at p sees j <= p, and with window > 0 only j > p - window or
+ *   j < sinks (the sequence's own first tokens, which stay visible)
+ *   o = sum_j softmax_j(softmax_scale q . k_j) v_j
+ * Query head h reads key/value head h / (H / Hkv).  A token that sees no key
+ * (a negative position: lens[row] < n_b) gives o = 0, lse = -infinity.
+ *
+ *   q          [T, H, d] dtype; k, v [T, Hkv, d] dtype or both NULL (the new
+ *              tokens are in their pages already)
+ *   cu_q       [B + 1] int32, non-decreasing, cu_q[B] <= T
+ *   row        [B] int32: the table row of each sequence, or NULL (row b).
+ *              Distinct when k is given, and no page of a sequence's new
+ *              tokens may then be held by another row (lizard_pages_fork
+ *              leaves it so)
+ *   o          [T, H, d] dtype, written; rows from cu_q[B] on are left as they were
+ *   lse        [T, H] fp32 natural-log softmax normaliser, or NULL
+ *   layer      which layer of the pool
+ *   max_q      upper bound of n_b (host value; selects the kernels)
+ *   1 <= H / Hkv <= 64, H a multiple of Hkv; softmax_scale 0 means 1/sqrt(d)
+ *   T = 0 or B = 0 is a no-op.
+ * fp32: portable kernels.  bf16: tensor-core kernels (impl AUTO or TC), with
+ * weights rounded to bf16 before their product with v, sums in fp32; or the
+ * portable ones (impl SIMT).
+ * Keys and values that no row may see have no effect, whatever they hold.
+ * Found on the device, LIZARD_ERR_INDEX is recorded in the workspace's
+ * status word (cleared by each call) for a sequence whose offsets, row,
+ * length (beyond max_pages * page) or number of tokens (beyond max_q) are
+ * not allowed, which is then left out, and for a page number outside the
+ * pool among the pages that a sequence's tokens see or go to (its output is
+ * then undefined; no memory outside the caller's arrays is touched).
+ */
+typedef struct {
+  int32_t layers, num_pages, Hkv, page, d;   /* the pool */
+  int32_t rows, max_pages;                   /* the table */
+  int32_t B, T, H, layer, max_q, window, sinks;
+  int32_t dtype;   /* lizard_dtype */
+  int32_t impl;    /* LIZARD_IMPL_* */
+  float softmax_scale;
+  const void *q, *k, *v;
+  void *k_pages, *v_pages;
+  const int32_t *table, *lens, *cu_q, *row;
+  void *o;
+  float *lse;
+  void *workspace;        /* >= lizard_paged_attn_workspace_size() bytes */
+  size_t workspace_bytes;
+} lizard_paged_args;
+
+/* Pointer fields are ignored.  Returns 0 when the sizes are invalid. */
+size_t lizard_paged_attn_workspace_size(const lizard_paged_args *args);
+lizard_status lizard_paged_attn(const lizard_paged_args *args, lizard_stream_t stream);
+
+/*
+ * The pages' bookkeeping, on the device and on the call's stream (so a
+ * captured graph replays it with the lengths of the moment).  Pages are
+ * handed out lowest number first, in the order of the call's list: the same
+ * calls give the same pages.  Each list names n table rows, all different.
+ *
+ * lizard_pages_reserve: row[i] grows by grow[i] >= 0 tokens: lens and the
+ *   table are extended, new pages get count 1.  The new slots' contents are
+ *   whatever the pages held.
+ * lizard_pages_free: row[i] gives up its tokens: the counts of its pages
+ *   drop by one, its table row becomes -1, its length 0.
+ * lizard_pages_fork: row[i] drops what it holds and continues from row
+ *   src[i] as that was before the call: the two share src's whole pages, and
+ *   a part-filled last page is copied (every layer, K and V) into a page
+ *   that was free before the call, so that each row may append to its own.
+ *   A src may occur many times and may itself be replaced by the same call;
+ *   row[i] == src[i] leaves the row as it is.
+ * lizard_pages_compact: the pool's L live pages move to numbers 0 .. L - 1
+ *   (the k-th live page with a number >= L goes to the k-th free number
+ *   below L; every layer, K and V), table_out and refs_out receive the table
+ *   and the counts with the new numbers.  They may be table and refs
+ *   themselves; otherwise those are left as they were (their pages beyond L
+ *   keep their contents until they are handed out again).  row, src, grow
+ *   and lens are not read.
+ *
+ * reserve, free and fork change everything or nothing: an index, length,
+ * duplicate row or held page that is not allowed (LIZARD_ERR_INDEX) or too
+ * few free pages (LIZARD_ERR_PAGES) is recorded in the workspace's status
+ * word, which each call clears first, and nothing is changed.  compact
+ * leaves a table entry that is not a live page (and not negative) as it is
+ * and records LIZARD_ERR_INDEX.  n = 0 is a no-op (compact does not read n).
+ * k_pages, v_pages, layers, Hkv, d and dtype are read by fork and compact
+ * only.
+ */
+typedef struct {
+  int32_t layers, num_pages, Hkv, page, d;   /* the pool */
+  int32_t rows, max_pages;                   /* the table */
+  int32_t dtype;   /* lizard_dtype */
+  int32_t n;       /* rows listed */
+  void *k_pages, *v_pages;
+  int32_t *refs, *table, *lens;
+  const int32_t *row, *src, *grow;
+  int32_t *table_out, *refs_out;
+  void *workspace;        /* >= lizard_pages_workspace_size() bytes */
+  size_t workspace_bytes;
+} lizard_pages_args;
+
+/* One size for all four calls with these sizes.  Pointer fields are ignored.
+ * Returns 0 when the sizes are invalid. */
+size_t lizard_pages_workspace_size(const lizard_pages_args *args);
+lizard_status lizard_pages_reserve(const lizard_pages_args *args, lizard_stream_t stream);
+lizard_status lizard_pages_free(const lizard_pages_args *args, lizard_stream_t stream);
+lizard_status lizard_pages_fork(const lizard_pages_args *args, lizard_stream_t stream);
+lizard_status lizard_pages_compact(const lizard_pages_args *args, lizard_stream_t stream);
+
+/*
  * Status of the decode steps run on the current device since the last call:
  * LIZARD_ERR_TIMEOUT when a step's bounded wait for its own copies gave up
  * (its outputs are then undefined), else LIZARD_OK; LIZARD_ERR_CUDA when
@@ -472,7 +604,8 @@ lizard_status lizard_noalloc_status(lizard_stream_t stream);
 
 /* Waits for `stream`, then reads and clears the status word that the last
  * forward or backward call left at the start of `workspace` (a device
- * pointer).  Returns LIZARD_OK, LIZARD_ERR_TIMEOUT or LIZARD_ERR_RANGE
+ * pointer).  Returns LIZARD_OK, LIZARD_ERR_TIMEOUT or LIZARD_ERR_RANGE, or
+ * after a paged-cache call LIZARD_ERR_INDEX or LIZARD_ERR_PAGES
  * (LIZARD_ERR_CUDA if the copy fails). */
 lizard_status lizard_workspace_status(void *workspace, lizard_stream_t stream);
 
