@@ -331,14 +331,15 @@ struct PagedArgs {
 // k, v into their pages.
 struct PagedGeometry {
   int few;                       // rows up to which a sequence belongs to class 0
-  int kt[2], tok[2], ctas[2];    // keys per tile, tokens per item, CTAs of each class
+  int kt[2], tok[2], ctas[2];    // keys per tile, tokens per item, CTAs (0: class not launched)
   int least[2];                  // fewest tiles a CTA takes
+  int slot_rows[2];              // rows of a partial slot
 };
 cudaError_t launch_paged_prep(const PagedArgs &a, const PagedGeometry &g, bool bf16, cudaStream_t s);
 cudaError_t launch_paged_simt(const PagedArgs &a, const PagedGeometry &g, bool bf16, cudaStream_t s);
-// Joins the pieces of split items (`slot_rows` rows per partial slot).
-cudaError_t launch_paged_join(const PagedArgs &a, const PagedGeometry &g, int cls, int slot_rows, bool bf16,
-                              cudaStream_t s);
+cudaError_t launch_paged_stream(const PagedArgs &a, const PagedGeometry &g, cudaStream_t s);   // class 0
+// Joins the pieces of both classes' split items.
+cudaError_t launch_paged_join(const PagedArgs &a, const PagedGeometry &g, bool bf16, cudaStream_t s);
 
 struct PagesArgs {
   int layers, num_pages, page, rows, max_pages, n;

@@ -46,37 +46,38 @@ lizard_status check_sizes(const lizard_paged_args *a) {
   return LIZARD_OK;
 }
 
-// Which kernels serve the call: the portable one for every sequence.
-struct Choice {
-  bool simt;
-  lz::PagedGeometry geo;
-  int slot_rows[2];
-};
-Choice choose(const lizard_paged_args *a) {
-  Choice c{};
+// The split of the batch over kernels.  bf16: sequences of at most
+// kStreamRows rows per key/value head go to the streaming kernel (class 0),
+// the others, when the call can have any, to the portable kernel (class 1);
+// fp32 and impl SIMT: all of them to the portable kernel.
+lz::PagedGeometry choose(const lizard_paged_args *a) {
+  lz::PagedGeometry c{};
   const int g = a->H / a->Hkv;
-  c.simt = true;
-  c.geo.few = 0;
-  c.geo.kt[0] = c.geo.kt[1] = 64;
-  c.geo.tok[0] = 1;
-  c.geo.tok[1] = lz::paged::kSimtRows / g;
-  c.geo.ctas[0] = 0;
-  c.geo.ctas[1] = lz::paged::kSimtCtas;
-  c.geo.least[0] = c.geo.least[1] = 2;
+  const bool tensor = a->dtype == LIZARD_BF16 && a->impl != LIZARD_IMPL_SIMT;
+  c.kt[0] = c.kt[1] = 64;
+  c.tok[0] = lz::paged::kStreamRows;
+  c.tok[1] = lz::paged::kSimtRows / g;
+  c.least[0] = c.least[1] = 2;
+  c.slot_rows[0] = lz::paged::kStreamRows;
   c.slot_rows[1] = lz::paged::kSimtRows;
+  if (tensor && g <= lz::paged::kStreamRows) {
+    c.few = lz::paged::kStreamRows;
+    c.ctas[0] = lz::paged::kStreamCtas;
+  }
+  if (!c.few || (long long)a->max_q * g > c.few) c.ctas[1] = lz::paged::kSimtCtas;
   return c;
 }
 
 struct PagedLayout {
   size_t split, prefix, part_o[2], part_ml[2], total;
 };
-PagedLayout paged_layout(const lizard_paged_args *a, const Choice &c) {
+PagedLayout paged_layout(const lizard_paged_args *a, const lz::PagedGeometry &c) {
   PagedLayout l{};
   size_t off = kHeader;
   l.split = off; off += up(2 * 2 * sizeof(long long));
   l.prefix = off; off += up(2 * ((size_t)a->B + 1) * sizeof(long long));
   for (int x = 0; x < 2; ++x) {
-    const size_t rows = 2 * (size_t)c.geo.ctas[x] * c.slot_rows[x];
+    const size_t rows = 2 * (size_t)c.ctas[x] * c.slot_rows[x];
     l.part_o[x] = off; off += up(rows * a->d * sizeof(float));
     l.part_ml[x] = off; off += up(rows * 2 * sizeof(float));
   }
@@ -104,7 +105,7 @@ lizard_status lizard_paged_attn(const lizard_paged_args *a, lizard_stream_t stre
                         a->o, a->lse, a->workspace};
   for (const void *p : ptrs)
     if (!ok_ptr(p)) return LIZARD_ERR_INVALID_ARG;
-  const Choice c = choose(a);
+  const lz::PagedGeometry c = choose(a);
   const PagedLayout lay = paged_layout(a, c);
   if (!a->workspace || a->workspace_bytes < lay.total) return LIZARD_ERR_WORKSPACE;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -131,9 +132,10 @@ lizard_status lizard_paged_attn(const lizard_paged_args *a, lizard_stream_t stre
     p.part_o[x] = at<float>(ws, lay.part_o[x]);
     p.part_ml[x] = at<float>(ws, lay.part_ml[x]);
   }
-  if (lz::launch_paged_prep(p, c.geo, bf16, s) != cudaSuccess) return LIZARD_ERR_CUDA;
-  if (lz::launch_paged_simt(p, c.geo, bf16, s) != cudaSuccess) return LIZARD_ERR_CUDA;
-  return cuda_status(lz::launch_paged_join(p, c.geo, 1, c.slot_rows[1], bf16, s));
+  if (lz::launch_paged_prep(p, c, bf16, s) != cudaSuccess) return LIZARD_ERR_CUDA;
+  if (c.ctas[0] && lz::launch_paged_stream(p, c, s) != cudaSuccess) return LIZARD_ERR_CUDA;
+  if (c.ctas[1] && lz::launch_paged_simt(p, c, bf16, s) != cudaSuccess) return LIZARD_ERR_CUDA;
+  return cuda_status(lz::launch_paged_join(p, c, bf16, s));
 }
 
 }  // extern "C"

@@ -80,7 +80,7 @@ __device__ void split_batch(const PagedArgs &a, const PagedGeometry &g) {
     for (int c = 0; c < 2; ++c) {
       a.prefix[(size_t)c * (a.B + 1) + a.B] = base[c];
       a.split[c].total = base[c];
-      const long long share = (base[c] + g.ctas[c] - 1) / g.ctas[c];
+      const long long n = g.ctas[c] > 0 ? g.ctas[c] : 1, share = (base[c] + n - 1) / n;
       a.split[c].share = share > g.least[c] ? share : g.least[c];
     }
   }
@@ -125,11 +125,10 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(PagedArgs a, P
 // before CTA x + 1 and acts when it is the first one inside an item; the rows
 // of the item go over blockIdx.y and the warps, a lane takes D / 32 columns.
 template <typename T, int D, int KT>
-__global__ void __launch_bounds__(256) paged_join_kernel(PagedArgs a, int cls, int tok, int slot_rows) {
+__device__ void join(const PagedArgs &a, const PagedGeometry &g, int cls) {
   constexpr int E = D / 32;
-  pdl_wait();
-  const int c = blockIdx.x + 1;
-  Cursor<KT> cur(a, cls, tok, c);
+  const int c = blockIdx.x + 1, slot_rows = g.slot_rows[cls];
+  Cursor<KT> cur(a, cls, g.tok[cls], c);
   if (!cur.valid() || cur.p.j0 == 0) return;
   const Split sp = a.split[cls];
   const long long begin = cur.u - cur.p.j0;
@@ -144,6 +143,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(PagedArgs a, int cls, i
     float m = kNoKey, l = 0.f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 4
     for (int x = first; x <= last; ++x) {
       const size_t at = (size_t)(x == first ? 2 * x + 1 : 2 * x) * slot_rows + r;
       const float2 v = ml[at];
@@ -164,12 +164,21 @@ __global__ void __launch_bounds__(256) paged_join_kernel(PagedArgs a, int cls, i
   }
 }
 
+// blockIdx.z: the class, counted from the first one that was launched.
 template <typename T, int D>
-cudaError_t launch_join(const PagedArgs &a, const PagedGeometry &g, int cls, int slot_rows, cudaStream_t s) {
-  const dim3 grid(g.ctas[cls] - 1, slot_rows >= 128 ? 8 : 2);
-  if (g.kt[cls] == 64)
-    return pdl_launch(paged_join_kernel<T, D, 64>, grid, 256, 0, s, a, cls, g.tok[cls], slot_rows);
-  return pdl_launch(paged_join_kernel<T, D, 128>, grid, 256, 0, s, a, cls, g.tok[cls], slot_rows);
+__global__ void __launch_bounds__(256) paged_join_kernel(PagedArgs a, PagedGeometry g) {
+  pdl_wait();
+  const int cls = g.ctas[0] ? blockIdx.z : 1;
+  if ((int)blockIdx.x + 1 >= g.ctas[cls]) return;
+  if (g.kt[cls] == 64) join<T, D, 64>(a, g, cls);
+  else join<T, D, 128>(a, g, cls);
+}
+
+template <typename T, int D> cudaError_t launch_join(const PagedArgs &a, const PagedGeometry &g, cudaStream_t s) {
+  const int most = g.ctas[0] > g.ctas[1] ? g.ctas[0] : g.ctas[1];
+  const int rows = g.ctas[1] ? g.slot_rows[1] : g.slot_rows[0];
+  const dim3 grid(most - 1, rows >= 128 ? 8 : 2, g.ctas[0] && g.ctas[1] ? 2 : 1);
+  return pdl_launch(paged_join_kernel<T, D>, grid, 256, 0, s, a, g);
 }
 
 }  // namespace
@@ -184,13 +193,9 @@ cudaError_t launch_paged_prep(const PagedArgs &a, const PagedGeometry &g, bool b
   return cudaGetLastError();
 }
 
-cudaError_t launch_paged_join(const PagedArgs &a, const PagedGeometry &g, int cls, int slot_rows, bool bf16,
-                              cudaStream_t s) {
-  if (bf16)
-    return a.d == 64 ? paged::launch_join<__nv_bfloat16, 64>(a, g, cls, slot_rows, s)
-                     : paged::launch_join<__nv_bfloat16, 128>(a, g, cls, slot_rows, s);
-  return a.d == 64 ? paged::launch_join<float, 64>(a, g, cls, slot_rows, s)
-                   : paged::launch_join<float, 128>(a, g, cls, slot_rows, s);
+cudaError_t launch_paged_join(const PagedArgs &a, const PagedGeometry &g, bool bf16, cudaStream_t s) {
+  if (bf16) return a.d == 64 ? paged::launch_join<__nv_bfloat16, 64>(a, g, s) : paged::launch_join<__nv_bfloat16, 128>(a, g, s);
+  return a.d == 64 ? paged::launch_join<float, 64>(a, g, s) : paged::launch_join<float, 128>(a, g, s);
 }
 
 }  // namespace lz

@@ -1,0 +1,295 @@
+// Paged attention for sequences with at most 16 rows per key/value head
+// (decoding, a few tokens at a time), bf16.
+//
+// Bound by reading the cache: every key and value is used by at most 16 rows,
+// 32 operations per byte.  So the kernel keeps loads in flight: a producer
+// warp fetches tiles of 64 keys (32 KB of K and V at d = 128) by TMA into a
+// ring of 3 (d = 128) or 6 stages, two CTAs per SM, which is 192 KB under way
+// per SM where about 45 KB cover the latency at full bandwidth.  The products
+// run on warp-level mma.sync m16n8k16: a tcgen05 tile has 128 rows, of which
+// 112 or more would be empty here, and its round trip through TMEM would be
+// longer than the 16 + 16 products that each of the four consumer warps needs
+// for its 16 keys of a tile.  Each warp keeps its own running maximum, sum
+// and output for its keys; they are joined once per piece.
+#include "paged_tma.cuh"
+
+namespace lz {
+namespace paged {
+namespace {
+
+constexpr int kKeys = 64, kWarps = 4, kThreads = (kWarps + 1) * 32;
+
+template <int D> constexpr int stages() { return D == 128 ? 3 : 6; }
+template <int D> constexpr uint32_t tile_bytes() { return kKeys * D * 2; }   // K or V
+template <int D> struct StreamSmem {
+  unsigned char kv[stages<D>()][2][tile_bytes<D>()];   // 64-column regions of 64 rows, 128-byte swizzle
+  float o[kStreamRows][D + 4];
+  float m[kWarps][kStreamRows], l[kWarps][kStreamRows];
+  uint64_t full[stages<D>()], empty[stages<D>()];
+  uint32_t dead;
+};
+
+LZ_DEV uint32_t kv_offset(int row, int chunk) {   // 16-byte chunk of a row
+  return (chunk >> 3) * (kKeys * 128) + tc::sw128_offset(row, (chunk & 7) * 8);
+}
+LZ_DEV void ldmatrix4(uint32_t addr, uint32_t *r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+LZ_DEV void ldmatrix4_t(uint32_t addr, uint32_t *r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+LZ_DEV void mma16816(float *c, const uint32_t *a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int D>
+__device__ void produce(const PagedArgs &a, const CUtensorMap *kmap, const CUtensorMap *vmap, StreamSmem<D> &sm,
+                        const Waits &wait) {
+  constexpr int S = stages<D>();
+  const int lane = threadIdx.x & 31;
+  const int box = min(a.page, 64), boxes = kKeys / box, per = boxes * (D / 64);
+  int it = 0;
+  for (Cursor<kKeys> cur(a, 0, kStreamRows, blockIdx.x); cur.valid(); cur.next()) {
+    const Piece &p = cur.p;
+    const Range range(a, p);
+    // lane i < 2 per loads box x of half `half` of K (i < per) or V
+    const int x = lane % per % boxes, half = lane % per / boxes;
+    const bool mine = lane < 2 * per;
+    int row = mine ? box_row(a, p, range, tile_index(p.t, p.j0) * kKeys + x * box, box) : 0;
+    for (int j = p.j0; j < p.j1; ++j, ++it) {
+      const int st = it % S;
+      if (it >= S) wait(&sm.empty[st], (it / S - 1) & 1);
+      if (*wait.dead) return;
+      if (lane == 0) tc::mbar_expect_tx(&sm.full[st], 2 * tile_bytes<D>());
+      __syncwarp();
+      if (mine)
+        tc::tma_load_3d(sm.kv[st][lane / per] + half * (kKeys * 128) + x * box * 128, lane < per ? kmap : vmap,
+                        &sm.full[st], half * 64, row, 0);
+      if (mine && j + 1 < p.j1) row = box_row(a, p, range, tile_index(p.t, j + 1) * kKeys + x * box, box);
+    }
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2)
+    paged_stream_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ CUtensorMap kmap,
+                        const __grid_constant__ CUtensorMap vmap) {
+  constexpr int S = stages<D>(), KS = D / 16, NT = D / 8;
+  extern __shared__ unsigned char raw[];
+  StreamSmem<D> &sm = *reinterpret_cast<StreamSmem<D> *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S; ++i) {
+      tc::mbar_init(&sm.full[i], 1);
+      tc::mbar_init(&sm.empty[i], kWarps);
+    }
+    sm.dead = 0;
+    tc::fence_barrier_init();
+  }
+  __syncthreads();
+  pdl_wait();
+  pdl_trigger();
+  const Waits wait{&sm.dead, a.status};
+  if (warp == kWarps) {
+    produce<D>(a, &kmap, &vmap, sm, wait);
+    return;
+  }
+  const Partial part{a.part_o[0], reinterpret_cast<float2 *>(a.part_ml[0])};
+  const float sc = a.scale * kLog2e;
+  const int r0 = lane >> 2, c0 = (lane & 3) * 2;       // fragment rows r0, r0 + 8; columns c0, c0 + 1
+  int it = 0;
+  for (Cursor<kKeys> cur(a, 0, kStreamRows, blockIdx.x); cur.valid(); cur.next()) {
+    const Piece &p = cur.p;
+    const Range range(a, p);
+    const int rows = (p.i1 - p.i0) * a.g, base = p.q.s - p.q.n;
+    uint32_t qf[KS][4];
+    int pos[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int r = r0 + 8 * x;
+      pos[x] = r < rows ? base + p.i0 + r / a.g : -1;
+      const uint32_t *q = reinterpret_cast<const uint32_t *>(
+          static_cast<const __nv_bfloat16 *>(a.q) +
+          ((size_t)(p.q.t0 + p.i0 + (r < rows ? r / a.g : 0)) * a.H + p.h * a.g + (r < rows ? r % a.g : 0)) * D + c0);
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        qf[k][x] = r < rows ? q[k * 8] : 0u;
+        qf[k][2 + x] = r < rows ? q[k * 8 + 4] : 0u;
+      }
+    }
+    float o[NT][4], m[2] = {kNoKey, kNoKey}, l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+    const int first_pos = base + p.i0, last_pos = base + p.i1 - 1;
+    for (int j = p.j0; j < p.j1; ++j, ++it) {
+      const int st = it % S, k0 = tile_index(p.t, j) * kKeys, kw = k0 + warp * 16;   // this warp's first key
+      wait(&sm.full[st], (it / S) & 1);
+      const uint32_t ka = tc::smem_u32(sm.kv[st][0]), va = tc::smem_u32(sm.kv[st][1]);
+      if (!range.whole(kw, 16)) {
+        // values that no row sees may be anything: their weight is zero, so make them zero
+        for (int x = lane; x < 16 * (D / 8); x += 32)
+          if (!range.any(kw + x / (D / 8)))
+            *reinterpret_cast<uint4 *>(sm.kv[st][1] + kv_offset(warp * 16 + x / (D / 8), x % (D / 8))) =
+                make_uint4(0, 0, 0, 0);
+        tc::fence_proxy_async();
+        __syncwarp();
+      }
+      float s[2][4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+#pragma unroll
+        for (int k = 0; k < KS; k += 2) {
+          uint32_t b[4];
+          ldmatrix4(ka + kv_offset(warp * 16 + n * 8 + (lane & 7), k * 2 + (lane >> 3)), b);
+          mma16816(s[n], qf[k], b[0], b[1]);
+          mma16816(s[n], qf[k + 1], b[2], b[3]);
+        }
+      }
+      const bool all = kw + 15 <= first_pos && (a.window == 0 || kw > last_pos - a.window || kw + 15 < a.sinks);
+      float mn[2] = {m[0], m[1]};
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float x = s[n][e] * sc;
+          if (!all && !sees(a, pos[e >> 1], kw + n * 8 + c0 + (e & 1))) x = -INFINITY;
+          s[n][e] = x;
+          mn[e >> 1] = x > mn[e >> 1] ? x : mn[e >> 1];
+        }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        mn[x] = fmaxf(mn[x], __shfl_xor_sync(0xffffffffu, mn[x], 1));
+        mn[x] = fmaxf(mn[x], __shfl_xor_sync(0xffffffffu, mn[x], 2));
+      }
+      if (__any_sync(0xffffffffu, mn[0] > m[0] || mn[1] > m[1])) {
+        const float f0 = exp2f(m[0] - mn[0]), f1 = exp2f(m[1] - mn[1]);
+        l[0] *= f0;
+        l[1] *= f1;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) o[n][0] *= f0, o[n][1] *= f0, o[n][2] *= f1, o[n][3] *= f1;
+        m[0] = mn[0];
+        m[1] = mn[1];
+      }
+      uint32_t pf[4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[n][e] = exp2f(s[n][e] - m[e >> 1]);
+          l[e >> 1] += s[n][e];
+        }
+        // weights go to the second product in bf16 (half a step, 2^-8 of each); the sum keeps 32 bits
+        pf[2 * n] = tc::pack_bf16(s[n][0], s[n][1]);
+        pf[2 * n + 1] = tc::pack_bf16(s[n][2], s[n][3]);
+      }
+#pragma unroll
+      for (int n = 0; n < NT; n += 2) {
+        uint32_t b[4];
+        ldmatrix4_t(va + kv_offset(warp * 16 + (lane & 15), n + (lane >> 4)), b);
+        mma16816(o[n], pf, b[0], b[1]);
+        mma16816(o[n + 1], pf, b[2], b[3]);
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sm.empty[st]);
+    }
+    // join the four warps: maxima and sums, then the outputs one warp at a time
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
+      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
+      if ((lane & 3) == 0) {
+        sm.m[warp][r0 + 8 * x] = m[x];
+        sm.l[warp][r0 + 8 * x] = l[x];
+      }
+    }
+    tc::bar_sync(1, kWarps * 32);
+    float f[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      float mm = kNoKey;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sm.m[w][r0 + 8 * x]);
+      f[x] = exp2f(m[x] - mm);
+    }
+    for (int w = 0; w < kWarps; ++w) {
+      if (w == warp) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (r0 + 8 * x >= rows) continue;
+            float2 *to = reinterpret_cast<float2 *>(&sm.o[r0 + 8 * x][n * 8 + c0]);
+            float2 v = make_float2(o[n][2 * x] * f[x], o[n][2 * x + 1] * f[x]);
+            if (w > 0) v.x += to->x, v.y += to->y;
+            *to = v;
+          }
+      }
+      tc::bar_sync(1, kWarps * 32);
+    }
+    constexpr int E = D / 32;
+    for (int r = warp; r < rows; r += kWarps) {
+      float mm = kNoKey, ll = 0.f, v[E];
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sm.m[w][r]);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) ll += sm.l[w][r] * exp2f(sm.m[w][r] - mm);
+      bool fine = isfinite(ll);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        v[e] = sm.o[r][lane * E + e];
+        fine = fine && isfinite(v[e]);
+      }
+      if (!__all_sync(0xffffffffu, fine)) {
+        exact_row_write<__nv_bfloat16, D>(a, p, kKeys, r, part, kStreamRows);
+        continue;
+      }
+      if (p.slot >= 0) {
+        const size_t at = (size_t)p.slot * kStreamRows + r;
+#pragma unroll
+        for (int e = 0; e < E; ++e) part.o[at * D + lane * E + e] = v[e];
+        if (lane == 0) part.ml[at] = make_float2(mm, ll);
+      } else {
+        const size_t at = (size_t)(p.q.t0 + p.i0 + r / a.g) * a.H + p.h * a.g + r % a.g;
+        const float inv = ll == 0.f ? 0.f : 1.f / ll;
+        uint32_t *to = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(a.o) + at * D + lane * E);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) to[e / 2] = tc::pack_bf16(v[e] * inv, v[e + 1] * inv);
+        if (a.lse && lane == 0) a.lse[at] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+      }
+    }
+    tc::bar_sync(1, kWarps * 32);       // before the next piece's maxima
+  }
+}
+
+template <int D> cudaError_t launch(const PagedArgs &a, const PagedGeometry &g, cudaStream_t s) {
+  CUtensorMap kmap, vmap;
+  if (!make_pool_map(&kmap, a.k_pages, a) || !make_pool_map(&vmap, a.v_pages, a)) return cudaErrorInvalidValue;
+  const size_t smem = sizeof(StreamSmem<D>) + 1024;
+  const cudaError_t e = cudaFuncSetAttribute(paged_stream_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)smem);
+  if (e != cudaSuccess) return e;
+  return pdl_launch(paged_stream_kernel<D>, g.ctas[0], kThreads, smem, s, a, kmap, vmap);
+}
+
+}  // namespace
+}  // namespace paged
+
+cudaError_t launch_paged_stream(const PagedArgs &a, const PagedGeometry &g, cudaStream_t s) {
+  return a.d == 64 ? paged::launch<64>(a, g, s) : paged::launch<128>(a, g, s);
+}
+
+}  // namespace lz
