@@ -338,6 +338,7 @@ struct PagedGeometry {
 cudaError_t launch_paged_prep(const PagedArgs &a, const PagedGeometry &g, bool bf16, cudaStream_t s);
 cudaError_t launch_paged_simt(const PagedArgs &a, const PagedGeometry &g, bool bf16, cudaStream_t s);
 cudaError_t launch_paged_stream(const PagedArgs &a, const PagedGeometry &g, cudaStream_t s);   // class 0
+cudaError_t launch_paged_tile(const PagedArgs &a, const PagedGeometry &g, cudaStream_t s);     // class 1
 // Joins the pieces of both classes' split items.
 cudaError_t launch_paged_join(const PagedArgs &a, const PagedGeometry &g, bool bf16, cudaStream_t s);
 

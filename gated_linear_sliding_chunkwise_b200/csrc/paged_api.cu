@@ -46,25 +46,38 @@ lizard_status check_sizes(const lizard_paged_args *a) {
   return LIZARD_OK;
 }
 
+bool on_tensor_cores(const lizard_paged_args *a) {
+  return a->dtype == LIZARD_BF16 && a->impl != LIZARD_IMPL_SIMT;
+}
+
 // The split of the batch over kernels.  bf16: sequences of at most
 // kStreamRows rows per key/value head go to the streaming kernel (class 0),
-// the others, when the call can have any, to the portable kernel (class 1);
-// fp32 and impl SIMT: all of them to the portable kernel.
+// the others, when the call can have any, to the tile kernel (class 1); fp32
+// and impl SIMT: all of them to the portable kernel (class 1).
 lz::PagedGeometry choose(const lizard_paged_args *a) {
   lz::PagedGeometry c{};
   const int g = a->H / a->Hkv;
-  const bool tensor = a->dtype == LIZARD_BF16 && a->impl != LIZARD_IMPL_SIMT;
-  c.kt[0] = c.kt[1] = 64;
-  c.tok[0] = lz::paged::kStreamRows;
-  c.tok[1] = lz::paged::kSimtRows / g;
   c.least[0] = c.least[1] = 2;
-  c.slot_rows[0] = lz::paged::kStreamRows;
-  c.slot_rows[1] = lz::paged::kSimtRows;
-  if (tensor && g <= lz::paged::kStreamRows) {
-    c.few = lz::paged::kStreamRows;
-    c.ctas[0] = lz::paged::kStreamCtas;
+  if (!on_tensor_cores(a)) {
+    c.kt[0] = c.kt[1] = 64;
+    c.tok[0] = c.tok[1] = lz::paged::kSimtRows / g;
+    c.ctas[1] = lz::paged::kSimtCtas;
+    c.slot_rows[1] = lz::paged::kSimtRows;
+    return c;
   }
-  if (!c.few || (long long)a->max_q * g > c.few) c.ctas[1] = lz::paged::kSimtCtas;
+  c.few = lz::paged::kStreamRows;
+  c.kt[0] = 64;
+  c.tok[0] = lz::paged::kStreamRows;
+  if (g <= c.few) {
+    c.ctas[0] = lz::paged::kStreamCtas;
+    c.slot_rows[0] = lz::paged::kStreamRows;
+  }
+  c.kt[1] = 128;
+  c.tok[1] = 2 * (lz::paged::kTileRows2 / 2 / g);
+  if ((long long)a->max_q * g > c.few) {
+    c.ctas[1] = lz::paged::kTileCtas;
+    c.slot_rows[1] = lz::paged::kTileRows2;
+  }
   return c;
 }
 
@@ -134,7 +147,9 @@ lizard_status lizard_paged_attn(const lizard_paged_args *a, lizard_stream_t stre
   }
   if (lz::launch_paged_prep(p, c, bf16, s) != cudaSuccess) return LIZARD_ERR_CUDA;
   if (c.ctas[0] && lz::launch_paged_stream(p, c, s) != cudaSuccess) return LIZARD_ERR_CUDA;
-  if (c.ctas[1] && lz::launch_paged_simt(p, c, bf16, s) != cudaSuccess) return LIZARD_ERR_CUDA;
+  if (c.ctas[1] &&
+      (on_tensor_cores(a) ? lz::launch_paged_tile(p, c, s) : lz::launch_paged_simt(p, c, bf16, s)) != cudaSuccess)
+    return LIZARD_ERR_CUDA;
   return cuda_status(lz::launch_paged_join(p, c, bf16, s));
 }
 

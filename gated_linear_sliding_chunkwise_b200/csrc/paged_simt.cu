@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(256, 2) paged_simt_kernel(PagedArgs a, int tok
       const unsigned odd = __ballot_sync(0xffffffffu, r < rows && !fine);
       for (int half = 0; half < 2; ++half)
         if (odd & (0xffffu << (16 * half)))
-          exact_row_write<T, D>(a, p, kKeys, ((tid >> 5) * 2 + half) * 4 + i, part, kRows);
+          exact_row_write<T, D>(a, Piece(p), kKeys, ((tid >> 5) * 2 + half) * 4 + i, part, kRows);
     }
   }
 }

@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         fine = fine && isfinite(v[e]);
       }
       if (!__all_sync(0xffffffffu, fine)) {
-        exact_row_write<__nv_bfloat16, D>(a, p, kKeys, r, part, kStreamRows);
+        exact_row_write<__nv_bfloat16, D>(a, Piece(p), kKeys, r, part, kStreamRows);
         continue;
       }
       if (p.slot >= 0) {

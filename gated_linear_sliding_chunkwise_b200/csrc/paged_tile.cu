@@ -1,0 +1,362 @@
+// Paged attention for sequences with more than 16 rows per key/value head
+// (chunks of prompts), bf16, on tcgen05.
+//
+// A CTA holds two 128-row query tiles of one (sequence, key/value head): rows
+// are (token, head of the group), so 128 / g tokens per tile.  Each tile has
+// its warpgroup, which owns its rows' softmax (thread = row = TMEM lane); one
+// warp loads, one issues the products.  Per tile of 128 keys:
+//
+//   load    K, V by TMA, a page (or 64 rows of it) per box, into a ring of
+//           tile-sized slots
+//   MMA     S_q = Q_q K^T                       (128 x 128, TMEM)
+//   rows    P_q = 2^(S scale log2 e - m) in bf16, over S_q's own columns;
+//           sums in fp32 from the unrounded weights
+//   MMA     O_q (+)= P_q V                      (128 x d, TMEM)
+//
+// The products of one query tile run while the other's rows are in the
+// softmax: PV_0(j), QK_0(j+1), PV_1(j), QK_1(j+1).  m is moved, and O
+// rescaled in TMEM, only when a row's maximum has grown by more than 2^8
+// since m was set: weights then stay below 2^8, well inside bf16 and fp32.
+// S_q(j+1) is issued after PV_q(j), so the barrier that announces S_q(j+1)
+// also says that O_q is complete up to j.
+//
+// Bound by the exponentials and the products about equally: 16384 weights
+// per (query tile, key tile) take 1024 cycles of the SM's 16 exp2 per cycle,
+// the two products 1024 cycles of the tensor pipe at d = 128.
+#include "paged_tma.cuh"
+
+namespace lz {
+namespace paged {
+namespace {
+
+constexpr int kKeys = 128, kThreads = 320;
+constexpr uint32_t kTmemCols = 512;
+constexpr float kSlack = 8.f;                     // log2 of the largest weight before m is moved
+
+template <int D> constexpr uint32_t tile_bytes() { return 128 * D * 2; }
+template <int D> constexpr int slots() { return D == 128 ? 5 : 10; }
+template <int D> struct TileSmem {
+  unsigned char q[2][tile_bytes<D>()];
+  unsigned char kv[slots<D>()][tile_bytes<D>()];  // K, V, K, V, ...
+  uint64_t q_full, q_empty, kv_full[slots<D>()], kv_empty[slots<D>()], s_full[2], p_full[2], o_full[2];
+  uint32_t tmem, dead;
+};
+
+LZ_DEV float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+// 32 lanes x 32-bit, 32 consecutive columns per thread.
+LZ_DEV void tmem_st32(uint32_t taddr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+// Tokens of query tile x of a piece: [i0 + x tpt, ...), `rows` rows.
+struct Half {
+  int first, tokens, rows;
+  LZ_DEV Half(const PagedArgs &a, const Piece &p, int tpt, int x) {
+    first = p.i0 + x * tpt;
+    tokens = max(0, min(tpt, p.i1 - first));
+    rows = tokens * a.g;
+  }
+};
+
+template <int D>
+__device__ void produce(const PagedArgs &a, const CUtensorMap *qmap, const CUtensorMap *kmap, const CUtensorMap *vmap,
+                        TileSmem<D> &sm, const Waits &wait, int tpt) {
+  constexpr int S = slots<D>();
+  const int lane = threadIdx.x & 31;
+  // K or V tile: lane < per loads box x of 64-column half `half`
+  const int box = min(a.page, 64), boxes = kKeys / box, per = boxes * (D / 64);
+  const int x = lane % boxes, half = lane / boxes;
+  const bool mine = lane < per;
+  int it = 0, pieces = 0;
+  for (Cursor<kKeys> cur(a, 1, 2 * tpt, blockIdx.x); cur.valid(); cur.next(), ++pieces) {
+    const Piece &p = cur.p;
+    const Range range(a, p);
+    if (pieces > 0) wait(&sm.q_empty, (pieces - 1) & 1);
+    if (*wait.dead) return;
+    if (lane == 0) {
+      const int halves = p.i0 + tpt < p.i1 ? 2 : 1;
+      tc::mbar_expect_tx(&sm.q_full, halves * tpt * a.g * D * 2);
+      for (int h = 0; h < halves; ++h)
+        for (int c = 0; c < D / 64; ++c)
+          tc::tma_load_3d(sm.q[h] + c * tc::kReg, qmap, &sm.q_full, c * 64, p.h * a.g, p.q.t0 + p.i0 + h * tpt);
+    }
+    __syncwarp();
+    int row = mine ? box_row(a, p, range, tile_index(p.t, p.j0) * kKeys + x * box, box) : 0;
+    for (int j = p.j0; j < p.j1; ++j) {
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv, ++it) {
+        const int st = it % S;
+        if (it >= S) wait(&sm.kv_empty[st], (it / S - 1) & 1);
+        if (*wait.dead) return;
+        if (lane == 0) tc::mbar_expect_tx(&sm.kv_full[st], tile_bytes<D>());
+        __syncwarp();
+        if (mine)
+          tc::tma_load_3d(sm.kv[st] + half * tc::kReg + x * box * 128, kv ? vmap : kmap, &sm.kv_full[st], half * 64,
+                          row, 0);
+      }
+      if (mine && j + 1 < p.j1) row = box_row(a, p, range, tile_index(p.t, j + 1) * kKeys + x * box, box);
+    }
+  }
+}
+
+template <int D>
+__device__ void multiply(const PagedArgs &a, TileSmem<D> &sm, const Waits &wait, uint32_t tmem, int tpt) {
+  constexpr int S = slots<D>();
+  constexpr uint32_t id_s = tc::idesc_bf16(128, 128, 0, 0), id_o = tc::idesc_bf16(128, D, 0, 1);
+  const int lane = threadIdx.x & 31;
+  uint32_t it = 0, pieces = 0, np[2] = {0, 0};
+  const auto qk = [&](int x, uint32_t k) {
+    if (lane != 0 || *wait.dead) return;
+    const uint32_t q = tc::smem_u32(sm.q[x]), kk = tc::smem_u32(sm.kv[k % S]);
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s)
+      tc::mma_ss(tmem + x * 128, tc::desc_k(q, s), tc::desc_k(kk, s), id_s, s > 0);
+    tc::mma_commit(&sm.s_full[x]);
+  };
+  const auto full = [&](uint32_t k) {
+    wait(&sm.kv_full[k % S], (k / S) & 1);
+    tc::tc_fence_after();
+  };
+  const auto release = [&](uint64_t *bar) {
+    if (lane == 0 && !*wait.dead) tc::mma_commit(bar);
+  };
+  for (Cursor<kKeys> cur(a, 1, 2 * tpt, blockIdx.x); cur.valid(); cur.next(), ++pieces) {
+    const Piece &p = cur.p;
+    const int halves = p.i0 + tpt < p.i1 ? 2 : 1;
+    wait(&sm.q_full, pieces & 1);
+    full(it);
+    for (int x = 0; x < halves; ++x) qk(x, it);
+    release(&sm.kv_empty[it % S]);
+    if (p.j1 - p.j0 == 1) release(&sm.q_empty);
+    for (int j = p.j0; j < p.j1; ++j, it += 2) {
+      const bool more = j + 1 < p.j1;
+      full(it + 1);
+      if (more) full(it + 2);
+      for (int x = 0; x < halves; ++x) {
+        wait(&sm.p_full[x], np[x]++ & 1);
+        tc::tc_fence_after();
+        if (lane == 0 && !*wait.dead) {
+          const uint32_t v = tc::smem_u32(sm.kv[(it + 1) % S]);
+#pragma unroll
+          for (int s = 0; s < kKeys / 16; ++s)
+            tc::mma_ts(tmem + 256 + x * 128, tmem + x * 128 + s * 8, tc::desc_mn(v, s), id_o, j > p.j0 || s > 0);
+          if (!more) tc::mma_commit(&sm.o_full[x]);
+        }
+        if (more) qk(x, it + 2);
+      }
+      release(&sm.kv_empty[(it + 1) % S]);
+      if (more) release(&sm.kv_empty[(it + 2) % S]);
+      if (more && j + 2 == p.j1) release(&sm.q_empty);
+    }
+  }
+}
+
+template <int D>
+__device__ void softmax(const PagedArgs &a, TileSmem<D> &sm, const Waits &wait, uint32_t tmem, int tpt) {
+  constexpr int S = slots<D>();
+  const int lane = threadIdx.x & 31, x = threadIdx.x >> 7, wrow = (threadIdx.x >> 5 & 3) * 32, row = wrow + lane;
+  const uint32_t lanes = (uint32_t)wrow << 16;
+  const uint32_t ts = tmem + lanes + x * 128, to = tmem + lanes + 256 + x * 128;
+  const Partial part{a.part_o[1], reinterpret_cast<float2 *>(a.part_ml[1])};
+  const float sc = a.scale * kLog2e;
+  uint32_t it = 0, ns = 0, no = 0;
+  for (Cursor<kKeys> cur(a, 1, 2 * tpt, blockIdx.x); cur.valid(); cur.next()) {
+    const Piece &p = cur.p;
+    const Half hf(a, p, tpt, x);
+    if (hf.rows == 0) {
+      it += 2 * (p.j1 - p.j0);
+      continue;
+    }
+    const Range range(a, p);
+    const int base = p.q.s - p.q.n, first = base + hf.first, last = first + hf.tokens - 1;
+    const int pos = row < hf.rows ? first + row / a.g : -1;
+    float m = kNoKey, l = 0.f;
+    for (int j = p.j0; j < p.j1; ++j, it += 2) {
+      const int k0 = tile_index(p.t, j) * kKeys;
+      if (!range.whole(k0, kKeys)) {
+        // values that no row sees may be anything: their weight is zero, so make them zero
+        const uint32_t v = it + 1;
+        wait(&sm.kv_full[v % S], (v / S) & 1);
+        for (int e = threadIdx.x & 127; e < kKeys * (D / 8); e += 128)
+          if (!range.any(k0 + e / (D / 8)))
+            *tc::chunk_ptr(sm.kv[v % S], 0, e / (D / 8), e % (D / 8)) = make_uint4(0, 0, 0, 0);
+        tc::fence_proxy_async();
+      }
+      wait(&sm.s_full[x], ns++ & 1);
+      tc::tc_fence_after();
+      if (wrow < hf.rows) {
+        float s[128];
+        tc::tmem_ld32x2(ts, ts + 32, s, s + 32);
+        tc::tmem_ld32x2(ts + 64, ts + 96, s + 64, s + 96);
+        const bool all = k0 + kKeys - 1 <= first &&
+                         (a.window == 0 || k0 > last - a.window || k0 + kKeys - 1 < a.sinks);
+        if (!all) {
+          const int hi = pos - k0, lo = a.window > 0 ? hi - a.window : INT_MIN, sk = a.window > 0 ? a.sinks - k0 : 0;
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (!(c <= hi && (c > lo || c < sk))) s[c] = -INFINITY;
+        }
+        float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int c = 4; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+        if (__any_sync(0xffffffffu, top > m + kSlack)) {
+          const float mn = fmaxf(m, top), f = ex2(m - mn);     // f = 0 at the first key
+          m = mn;
+          l *= f;
+          if (j > p.j0) {
+            float o[16];                     // few at a time: the row's 128 logits stay in registers
+#pragma unroll
+            for (int c = 0; c < D; c += 16) {
+              tc::tmem_ld16(to + c, o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] *= f;
+              tc::tmem_st8(to + c, reinterpret_cast<const uint32_t *>(o));
+              tc::tmem_st8(to + c + 8, reinterpret_cast<const uint32_t *>(o + 8));
+            }
+          }
+        }
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 128; c += 64) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int e = 0; e < 64; e += 2) {
+            const float w0 = ex2(fmaf(s[c + e], sc, -m)), w1 = ex2(fmaf(s[c + e + 1], sc, -m));
+            sum[(e >> 1) & 3] += w0 + w1;
+            // weights go to the second product in bf16 (half a step, 2^-8 of each); the sum keeps 32 bits
+            pk[e / 2] = tc::pack_bf16(w0, w1);
+          }
+          tmem_st32(ts + c / 2, pk);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tc::tmem_st_wait();
+      }
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sm.p_full[x]);
+    }
+    wait(&sm.o_full[x], no++ & 1);
+    tc::tc_fence_after();
+    if (wrow >= hf.rows) continue;
+    // out: 32 columns at a time, unnormalised sums for a split item
+    const int r = x * tpt * a.g + row;
+    const bool live = row < hf.rows;
+    const size_t at = p.slot >= 0 ? (size_t)p.slot * kTileRows2 + r
+                                  : (size_t)(p.q.t0 + p.i0 + r / a.g) * a.H + p.h * a.g + r % a.g;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    bool fine = isfinite(l);
+#pragma unroll
+    for (int c = 0; c < D; c += 32) {
+      float o[32];
+      tc::tmem_ld32(to + c, o);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) fine = fine && isfinite(o[e]);
+      if (!live) continue;
+      if (p.slot >= 0) {
+        float4 *out = reinterpret_cast<float4 *>(part.o + at * D + c);
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) out[e / 4] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+      } else {
+        uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + at * D + c);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] *= inv;
+#pragma unroll
+        for (int e = 0; e < 32; e += 8) out[e / 8] = tc::pack8(o + e);
+      }
+    }
+    if (live) {
+      if (p.slot >= 0) part.ml[at] = make_float2(m, l);
+      else if (a.lse) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    }
+    tc::tc_fence_before();
+    for (unsigned odd = __ballot_sync(0xffffffffu, live && !fine); odd; odd &= odd - 1)
+      exact_row_write<__nv_bfloat16, D>(a, Piece(p), kKeys, x * tpt * a.g + wrow + __ffs(odd) - 1, part, kTileRows2);
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_tile_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ CUtensorMap qmap,
+                      const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, int tpt) {
+  constexpr int S = slots<D>();
+  extern __shared__ unsigned char raw[];
+  TileSmem<D> &sm = *reinterpret_cast<TileSmem<D> *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    tc::mbar_init(&sm.q_full, 1);
+    tc::mbar_init(&sm.q_empty, 1);
+    for (int i = 0; i < S; ++i) {
+      tc::mbar_init(&sm.kv_full[i], 1);
+      tc::mbar_init(&sm.kv_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&sm.s_full[i], 1);
+      tc::mbar_init(&sm.p_full[i], 4);
+      tc::mbar_init(&sm.o_full[i], 1);
+    }
+    sm.dead = 0;
+    tc::fence_barrier_init();
+  }
+  if (warp == 9) {
+    tc::tmem_alloc(&sm.tmem, kTmemCols);
+    tc::tmem_relinquish();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  pdl_wait();
+  pdl_trigger();
+  const uint32_t tmem = sm.tmem;
+  const Waits wait{&sm.dead, a.status};
+  if (warp < 8) softmax<D>(a, sm, wait, tmem, tpt);
+  else if (warp == 8) produce<D>(a, &qmap, &kmap, &vmap, sm, wait, tpt);
+  else multiply<D>(a, sm, wait, tmem, tpt);
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == 9) tc::tmem_dealloc(tmem, kTmemCols);
+}
+
+// q [T][H][d]: a box is 64 columns x the g heads of a group x tpt tokens.
+bool make_query_map(CUtensorMap *map, const PagedArgs &a, int tpt) {
+  tc::EncodeTiledFn fn = tc::encode_tiled_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)a.d, (cuuint64_t)a.H, (cuuint64_t)a.T};
+  const cuuint64_t strides[2] = {(cuuint64_t)a.d * 2, (cuuint64_t)a.H * a.d * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)a.g, (cuuint32_t)tpt}, estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(a.q), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D> cudaError_t launch(const PagedArgs &a, const PagedGeometry &g, cudaStream_t s) {
+  CUtensorMap qmap, kmap, vmap;
+  const int tpt = g.tok[1] / 2;
+  if (!make_query_map(&qmap, a, tpt) || !make_pool_map(&kmap, a.k_pages, a) || !make_pool_map(&vmap, a.v_pages, a))
+    return cudaErrorInvalidValue;
+  const size_t smem = sizeof(TileSmem<D>) + 1024;
+  const cudaError_t e = cudaFuncSetAttribute(paged_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)smem);
+  if (e != cudaSuccess) return e;
+  return pdl_launch(paged_tile_kernel<D>, g.ctas[1], kThreads, smem, s, a, qmap, kmap, vmap, tpt);
+}
+
+}  // namespace
+}  // namespace paged
+
+cudaError_t launch_paged_tile(const PagedArgs &a, const PagedGeometry &g, cudaStream_t s) {
+  return a.d == 64 ? paged::launch<64>(a, g, s) : paged::launch<128>(a, g, s);
+}
+
+}  // namespace lz
