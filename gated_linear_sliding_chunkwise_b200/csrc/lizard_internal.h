@@ -303,6 +303,8 @@ cudaError_t launch_finish_bwd(const FinishBwdArgs &a, int BH, int D, bool bf16, 
 // ------------------------------------------------------ paged cache -------
 namespace paged {
 struct Split;
+struct Seq;
+struct JoinItem;
 constexpr int kSMs = 148;                       // SMs of a B200
 // CTAs that share a class's work: portable and streaming kernels two per SM,
 // the tile kernel one.
@@ -322,6 +324,8 @@ struct PagedArgs {
   uint32_t *status;
   paged::Split *split;           // [2]
   long long *prefix;             // [2][B + 1]
+  paged::Seq *seqs;              // [B]
+  paged::JoinItem *items[2];     // [CTAs of the class]
   // partial sums per class: [slots][rows][d] fp32 and [slots][rows] (maximum, sum)
   float *part_o[2];
   float *part_ml[2];

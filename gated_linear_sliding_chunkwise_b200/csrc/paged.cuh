@@ -50,12 +50,13 @@ cudaError_t pdl_launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem
 }
 
 // ------------------------------------------------------------ sequences ---
-struct Seq {
+struct __align__(16) Seq {
   int t0, n, s, row;   // first new token in q, new tokens, length with them, table row
 };
-// Sequence b of the batch; n = 0 when there is nothing to do or something is
-// not allowed (`bad` says so).
-LZ_DEV Seq get_seq(const PagedArgs &a, int b, bool *bad = nullptr) {
+// Sequence b of the batch, checked; n = 0 when there is nothing to do or
+// something is not allowed (`bad` says so).  The prep kernel keeps the result
+// in a.seqs for the kernels after it.
+LZ_DEV Seq check_seq(const PagedArgs &a, int b, bool *bad = nullptr) {
   Seq q;
   const int t0 = a.cu_q[b], t1 = a.cu_q[b + 1];
   const int row = a.row ? a.row[b] : b;
@@ -129,6 +130,12 @@ struct Piece {
 // Whether a sequence of n tokens belongs to class 0 (few rows).
 LZ_DEV bool few_rows(const PagedArgs &a, int n, int few) { return n * a.g <= few; }
 
+// Item that begins in CTA c's stretch and goes on in those up to CTA `last`:
+// entry c of a.items[class], rows = 0 when there is none.
+struct __align__(16) JoinItem {
+  int token, head, rows, last;
+};
+
 // Walks the pieces of one CTA's stretch.  All lanes of a warp call it
 // together (the first search runs across the lanes).
 template <int KT>
@@ -136,53 +143,73 @@ struct Cursor {
   const PagedArgs &a;
   const long long *prefix;
   int tok;               // tokens per item
-  long long u, end;
+  long long u, end, share;
   int cta;
   Piece p;
   int nitem;
+  // Latency counts here: every CTA starts with it.  The search for the
+  // sequence probes 32 places at a time (one step for 32 sequences, two for
+  // 1024), and its first probes do not wait for the split.
   LZ_DEV Cursor(const PagedArgs &a_, int cls, int tok_, int cta_) : a(a_), tok(tok_), cta(cta_) {
+    const int lane = threadIdx.x & 31;
     prefix = a.prefix + (size_t)cls * (a.B + 1);
+    int lo = 0, width = a.B;                      // the sequence is one of lo .. lo + width - 1
+    int step = (width + 31) / 32;
+    long long probe = prefix[min(lane * step, a.B)];
     const Split sp = a.split[cls];
-    u = sp.share * cta;
-    end = min(u + sp.share, sp.total);
+    share = sp.share;
+    u = share * cta;
+    end = min(u + share, sp.total);
     if (u >= end) return;
-    int lo = 0, hi = a.B;                         // prefix[lo] <= u < prefix[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (prefix[mid] <= u) lo = mid; else hi = mid;
+    for (;;) {
+      // the last probed place that does not lie behind u (empty sequences share a place with the next)
+      const unsigned below = __ballot_sync(0xffffffffu, lane * step < width && probe <= u);
+      const int l = 31 - __clz(below);
+      lo += l * step;
+      width = min(step, width - l * step);
+      if (width <= 1) break;
+      step = (width + 31) / 32;
+      probe = prefix[min(lo + lane * step, a.B)];
     }
     p.b = lo;
+    const long long before = prefix[lo], all_tiles = prefix[lo + 1] - before;
     open_seq();
-    const long long per = (prefix[lo + 1] - prefix[lo]) / a.Hkv;
-    long long rem = u - prefix[lo];
-    p.h = (int)(rem / per);
-    rem -= p.h * per;
-    // the item: 32 at a time
-    const int lane = threadIdx.x & 31;
-    int it = 0;
-    for (;; it += 32) {
-      int c = 0;
-      if (it + lane < nitem) {
-        const int i0 = (it + lane) * tok;
-        c = tiles_of<KT>(a, p.q, i0, min(i0 + tok, p.q.n)).count;
-      }
-      int pre = c;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, pre, o);
-        if (lane >= o) pre += x;
-      }
-      const int all = __shfl_sync(0xffffffffu, pre, 31);
-      if (rem >= all && it + 32 < nitem) {
-        rem -= all;
-        continue;
-      }
-      const unsigned past = __ballot_sync(0xffffffffu, rem < pre);
-      const int l = past ? __ffs(past) - 1 : 0;
-      rem -= __shfl_sync(0xffffffffu, pre - c, l);
-      it += l;
-      break;
+    long long rem = u - before;
+    if (all_tiles < INT_MAX) {                    // 32-bit division where it does
+      const unsigned per = (unsigned)all_tiles / (unsigned)a.Hkv;
+      p.h = (unsigned)rem / per;
+      rem = (unsigned)rem % per;
+    } else {
+      const long long per = all_tiles / a.Hkv;
+      p.h = (int)(rem / per);
+      rem %= per;
     }
+    // the item: 32 at a time
+    int it = 0;
+    if (nitem > 1)
+      for (;; it += 32) {
+        int c = 0;
+        if (it + lane < nitem) {
+          const int i0 = (it + lane) * tok;
+          c = tiles_of<KT>(a, p.q, i0, min(i0 + tok, p.q.n)).count;
+        }
+        int pre = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int x = __shfl_up_sync(0xffffffffu, pre, o);
+          if (lane >= o) pre += x;
+        }
+        const int all = __shfl_sync(0xffffffffu, pre, 31);
+        if (rem >= all && it + 32 < nitem) {
+          rem -= all;
+          continue;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, rem < pre);
+        const int l = past ? __ffs(past) - 1 : 0;
+        rem -= __shfl_sync(0xffffffffu, pre - c, l);
+        it += l;
+        break;
+      }
     p.item = it;
     open_item((int)rem);
   }
@@ -201,10 +228,22 @@ struct Cursor {
     }
     open_item(0);
   }
+  // What the join kernel needs to know of a split item that begins in this
+  // CTA's stretch (always its last piece).
+  LZ_DEV JoinItem join_item() const {
+    JoinItem d{};
+    if (p.slot == 2 * cta + 1) {
+      d.rows = (p.i1 - p.i0) * a.g;
+      d.token = p.q.t0 + p.i0;
+      d.head = p.h * a.g;
+      d.last = (int)((u + p.t.count - 1) / share);
+    }
+    return d;
+  }
 
  private:
   LZ_DEV void open_seq() {
-    p.q = get_seq(a, p.b);
+    p.q = a.seqs[p.b];
     nitem = (p.q.n + tok - 1) / tok;
   }
   LZ_DEV void open_item(int j0) {

@@ -82,14 +82,16 @@ lz::PagedGeometry choose(const lizard_paged_args *a) {
 }
 
 struct PagedLayout {
-  size_t split, prefix, part_o[2], part_ml[2], total;
+  size_t split, prefix, seqs, items[2], part_o[2], part_ml[2], total;
 };
 PagedLayout paged_layout(const lizard_paged_args *a, const lz::PagedGeometry &c) {
   PagedLayout l{};
   size_t off = kHeader;
   l.split = off; off += up(2 * 2 * sizeof(long long));
   l.prefix = off; off += up(2 * ((size_t)a->B + 1) * sizeof(long long));
+  l.seqs = off; off += up((size_t)a->B * 4 * sizeof(int));
   for (int x = 0; x < 2; ++x) {
+    l.items[x] = off; off += up((size_t)c.ctas[x] * 4 * sizeof(int));
     const size_t rows = 2 * (size_t)c.ctas[x] * c.slot_rows[x];
     l.part_o[x] = off; off += up(rows * a->d * sizeof(float));
     l.part_ml[x] = off; off += up(rows * 2 * sizeof(float));
@@ -141,7 +143,9 @@ lizard_status lizard_paged_attn(const lizard_paged_args *a, lizard_stream_t stre
   p.status = static_cast<uint32_t *>(ws);
   p.split = at<lz::paged::Split>(ws, lay.split);
   p.prefix = at<long long>(ws, lay.prefix);
+  p.seqs = at<lz::paged::Seq>(ws, lay.seqs);
   for (int x = 0; x < 2; ++x) {
+    p.items[x] = at<lz::paged::JoinItem>(ws, lay.items[x]);
     p.part_o[x] = at<float>(ws, lay.part_o[x]);
     p.part_ml[x] = at<float>(ws, lay.part_ml[x]);
   }

@@ -29,7 +29,10 @@ __device__ void split_batch(const PagedArgs &a, const PagedGeometry &g) {
     const int b = b0 + threadIdx.x;
     Seq q{};
     bool bad = false;
-    if (b < a.B) q = get_seq(a, b, &bad);
+    if (b < a.B) {
+      q = check_seq(a, b, &bad);
+      a.seqs[b] = q;
+    }
     any_bad |= bad;
     const int cls = few_rows(a, q.n, g.few) ? 0 : 1;
     const int nitem = q.n > 0 ? (q.n + g.tok[cls] - 1) / g.tok[cls] : 0;
@@ -107,7 +110,7 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(PagedArgs a, P
       if (a.cu_q[mid] <= t) lo = mid; else hi = mid;
     }
   }
-  const Seq q = get_seq(a, lo);
+  const Seq q = check_seq(a, lo);
   const int i = t - q.t0;
   if (i < 0 || i >= q.n) return;               // between or behind the sequences
   const int p = q.s - q.n + i;
@@ -121,30 +124,23 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(PagedArgs a, P
 }
 
 // Joins a split item's pieces: o = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i
-// over the CTAs that the item spans, in order.  Block x looks at the boundary
-// before CTA x + 1 and acts when it is the first one inside an item; the rows
-// of the item go over blockIdx.y and the warps, a lane takes D / 32 columns.
-template <typename T, int D, int KT>
+// over the CTAs that the item spans, in order.  Block x takes the item that
+// begins in CTA x's stretch, if one does; its rows go over blockIdx.y and the
+// warps, a lane takes D / 32 columns.
+template <typename T, int D>
 __device__ void join(const PagedArgs &a, const PagedGeometry &g, int cls) {
   constexpr int E = D / 32;
-  const int c = blockIdx.x + 1, slot_rows = g.slot_rows[cls];
-  Cursor<KT> cur(a, cls, g.tok[cls], c);
-  if (!cur.valid() || cur.p.j0 == 0) return;
-  const Split sp = a.split[cls];
-  const long long begin = cur.u - cur.p.j0;
-  const int first = (int)(begin / sp.share);
-  if (c != first + 1) return;
-  const int last = (int)((begin + cur.p.t.count - 1) / sp.share);
-  const int rows = (cur.p.i1 - cur.p.i0) * a.g;
+  const int first = blockIdx.x, slot_rows = g.slot_rows[cls];
+  const JoinItem d = a.items[cls][first];
   const int lane = threadIdx.x & 31;
   const float *po = a.part_o[cls];
   const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml[cls]);
-  for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < rows; r += gridDim.y * 8) {
+  for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < d.rows; r += gridDim.y * 8) {
     float m = kNoKey, l = 0.f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
 #pragma unroll 4
-    for (int x = first; x <= last; ++x) {
+    for (int x = first; x <= d.last; ++x) {
       const size_t at = (size_t)(x == first ? 2 * x + 1 : 2 * x) * slot_rows + r;
       const float2 v = ml[at];
       const float mn = v.x > m ? v.x : m;
@@ -154,8 +150,7 @@ __device__ void join(const PagedArgs &a, const PagedGeometry &g, int cls) {
       for (int e = 0; e < E; ++e) acc[e] = acc[e] * fo + po[at * D + lane * E + e] * fn;
       m = mn;
     }
-    const int i = cur.p.i0 + r / a.g, head = cur.p.h * a.g + r % a.g;
-    const size_t at = (size_t)(cur.p.q.t0 + i) * a.H + head;
+    const size_t at = (size_t)(d.token + r / a.g) * a.H + d.head + r % a.g;
     const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
     for (int e = 0; e < E; ++e)
@@ -169,15 +164,13 @@ template <typename T, int D>
 __global__ void __launch_bounds__(256) paged_join_kernel(PagedArgs a, PagedGeometry g) {
   pdl_wait();
   const int cls = g.ctas[0] ? blockIdx.z : 1;
-  if ((int)blockIdx.x + 1 >= g.ctas[cls]) return;
-  if (g.kt[cls] == 64) join<T, D, 64>(a, g, cls);
-  else join<T, D, 128>(a, g, cls);
+  if ((int)blockIdx.x + 1 < g.ctas[cls]) join<T, D>(a, g, cls);
 }
 
 template <typename T, int D> cudaError_t launch_join(const PagedArgs &a, const PagedGeometry &g, cudaStream_t s) {
   const int most = g.ctas[0] > g.ctas[1] ? g.ctas[0] : g.ctas[1];
   const int rows = g.ctas[1] ? g.slot_rows[1] : g.slot_rows[0];
-  const dim3 grid(most - 1, rows >= 128 ? 8 : 2, g.ctas[0] && g.ctas[1] ? 2 : 1);
+  const dim3 grid(most - 1, (rows + 31) / 32, g.ctas[0] && g.ctas[1] ? 2 : 1);
   return pdl_launch(paged_join_kernel<T, D>, grid, 256, 0, s, a, g);
 }
 

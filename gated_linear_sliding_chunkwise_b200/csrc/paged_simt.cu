@@ -45,8 +45,10 @@ __global__ void __launch_bounds__(256, 2) paged_simt_kernel(PagedArgs a, int tok
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const Partial part{a.part_o[1], reinterpret_cast<float2 *>(a.part_ml[1])};
   const float sc = a.scale * kLog2e;
+  JoinItem item{};
   for (Cursor<kKeys> cur(a, 1, tok, blockIdx.x); cur.valid(); cur.next()) {
     const Piece &p = cur.p;
+    item = cur.join_item();
     const int rows = (p.i1 - p.i0) * a.g, base = p.q.s - p.q.n;
     __syncthreads();                        // the last piece's reads of q
     for (int x = tid; x < kRows * D / 4; x += 256) {
@@ -184,6 +186,7 @@ __global__ void __launch_bounds__(256, 2) paged_simt_kernel(PagedArgs a, int tok
           exact_row_write<T, D>(a, Piece(p), kKeys, ((tid >> 5) * 2 + half) * 4 + i, part, kRows);
     }
   }
+  if (tid == 0) a.items[1][blockIdx.x] = item;
 }
 
 template <typename T, int D>

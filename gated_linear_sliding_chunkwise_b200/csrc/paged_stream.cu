@@ -9,8 +9,11 @@
 // run on warp-level mma.sync m16n8k16: a tcgen05 tile has 128 rows, of which
 // 112 or more would be empty here, and its round trip through TMEM would be
 // longer than the 16 + 16 products that each of the four consumer warps needs
-// for its 16 keys of a tile.  Each warp keeps its own running maximum, sum
-// and output for its keys; they are joined once per piece.
+// per tile.  A warp takes 16 of the tile's keys in the first product and D / 4
+// of the columns in the second, with the maxima and the weights handed over
+// in shared memory (two barriers of 128 threads a tile): no warp holds another
+// sum for the same output, so a piece ends without a join of the warps, which
+// took 4.6 us of a call with one token.
 #include "paged_tma.cuh"
 
 namespace lz {
@@ -23,8 +26,9 @@ template <int D> constexpr int stages() { return D == 128 ? 3 : 6; }
 template <int D> constexpr uint32_t tile_bytes() { return kKeys * D * 2; }   // K or V
 template <int D> struct StreamSmem {
   unsigned char kv[stages<D>()][2][tile_bytes<D>()];   // 64-column regions of 64 rows, 128-byte swizzle
-  float o[kStreamRows][D + 4];
+  unsigned char p[kStreamRows * 128];                  // weights, bf16 [row][key], 128-byte swizzle
   float m[kWarps][kStreamRows], l[kWarps][kStreamRows];
+  uint32_t odd[kWarps];
   uint64_t full[stages<D>()], empty[stages<D>()];
   uint32_t dead;
 };
@@ -84,7 +88,7 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 2)
     paged_stream_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ CUtensorMap vmap) {
-  constexpr int S = stages<D>(), KS = D / 16, NT = D / 8;
+  constexpr int S = stages<D>(), KS = D / 16, NT = D / 8 / kWarps;   // NT: 8-column blocks of this warp
   extern __shared__ unsigned char raw[];
   StreamSmem<D> &sm = *reinterpret_cast<StreamSmem<D> *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -108,8 +112,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   const float sc = a.scale * kLog2e;
   const int r0 = lane >> 2, c0 = (lane & 3) * 2;       // fragment rows r0, r0 + 8; columns c0, c0 + 1
   int it = 0;
+  JoinItem item{};
   for (Cursor<kKeys> cur(a, 0, kStreamRows, blockIdx.x); cur.valid(); cur.next()) {
     const Piece &p = cur.p;
+    item = cur.join_item();
     const Range range(a, p);
     const int rows = (p.i1 - p.i0) * a.g, base = p.q.s - p.q.n;
     uint32_t qf[KS][4];
@@ -143,8 +149,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (!range.any(kw + x / (D / 8)))
             *reinterpret_cast<uint4 *>(sm.kv[st][1] + kv_offset(warp * 16 + x / (D / 8), x % (D / 8))) =
                 make_uint4(0, 0, 0, 0);
-        tc::fence_proxy_async();
-        __syncwarp();
+        tc::fence_proxy_async();       // before the stage is loaded again
       }
       float s[2][4];
 #pragma unroll
@@ -160,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
       const bool all = kw + 15 <= first_pos && (a.window == 0 || kw > last_pos - a.window || kw + 15 < a.sinks);
-      float mn[2] = {m[0], m[1]};
+      float mn[2] = {kNoKey, kNoKey};
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -168,111 +173,102 @@ __global__ void __launch_bounds__(kThreads, 2)
           float x = s[n][e] * sc;
           if (!all && !sees(a, pos[e >> 1], kw + n * 8 + c0 + (e & 1))) x = -INFINITY;
           s[n][e] = x;
-          mn[e >> 1] = x > mn[e >> 1] ? x : mn[e >> 1];
+          mn[e >> 1] = fmaxf(mn[e >> 1], x);
         }
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         mn[x] = fmaxf(mn[x], __shfl_xor_sync(0xffffffffu, mn[x], 1));
         mn[x] = fmaxf(mn[x], __shfl_xor_sync(0xffffffffu, mn[x], 2));
+        if ((lane & 3) == 0) sm.m[warp][r0 + 8 * x] = mn[x];
       }
-      if (__any_sync(0xffffffffu, mn[0] > m[0] || mn[1] > m[1])) {
-        const float f0 = exp2f(m[0] - mn[0]), f1 = exp2f(m[1] - mn[1]);
-        l[0] *= f0;
-        l[1] *= f1;
+      // every warp has read the last tile's maxima and weights
+      tc::bar_sync(1, kWarps * 32);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) o[n][0] *= f0, o[n][1] *= f0, o[n][2] *= f1, o[n][3] *= f1;
-        m[0] = mn[0];
-        m[1] = mn[1];
-      }
-      uint32_t pf[4];
+      for (int x = 0; x < 2; ++x) {
+        mn[x] = m[x];
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
+        for (int w = 0; w < kWarps; ++w) mn[x] = fmaxf(mn[x], sm.m[w][r0 + 8 * x]);
+        const float f = exp2f(m[x] - mn[x]);
+        m[x] = mn[x];
+        l[x] *= f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          s[n][e] = exp2f(s[n][e] - m[e >> 1]);
-          l[e >> 1] += s[n][e];
+        for (int n = 0; n < NT; ++n) o[n][2 * x] *= f, o[n][2 * x + 1] *= f;
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const float w0 = exp2f(s[n][2 * x] - m[x]), w1 = exp2f(s[n][2 * x + 1] - m[x]);
+          l[x] += w0 + w1;
+          // weights go to the second product in bf16 (half a step, 2^-8 of each); the sum keeps 32 bits
+          *reinterpret_cast<uint32_t *>(sm.p + tc::sw128_offset(r0 + 8 * x, warp * 16 + n * 8 + c0)) =
+              tc::pack_bf16(w0, w1);
         }
-        // weights go to the second product in bf16 (half a step, 2^-8 of each); the sum keeps 32 bits
-        pf[2 * n] = tc::pack_bf16(s[n][0], s[n][1]);
-        pf[2 * n + 1] = tc::pack_bf16(s[n][2], s[n][3]);
       }
+      tc::bar_sync(1, kWarps * 32);
 #pragma unroll
-      for (int n = 0; n < NT; n += 2) {
-        uint32_t b[4];
-        ldmatrix4_t(va + kv_offset(warp * 16 + (lane & 15), n + (lane >> 4)), b);
-        mma16816(o[n], pf, b[0], b[1]);
-        mma16816(o[n + 1], pf, b[2], b[3]);
+      for (int k = 0; k < kKeys / 16; ++k) {
+        uint32_t pf[4];
+        ldmatrix4(tc::smem_u32(sm.p) + tc::sw128_offset(lane & 15, k * 16 + (lane >> 4) * 8), pf);
+#pragma unroll
+        for (int n = 0; n < NT; n += 2) {
+          uint32_t b[4];
+          ldmatrix4_t(va + kv_offset(k * 16 + (lane & 15), warp * NT + n + (lane >> 4)), b);
+          mma16816(o[n], pf, b[0], b[1]);
+          mma16816(o[n + 1], pf, b[2], b[3]);
+        }
       }
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&sm.empty[st]);
     }
-    // join the four warps: maxima and sums, then the outputs one warp at a time
+    // the sum over the warps' keys; the output's columns are this warp's own
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
       l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
-      if ((lane & 3) == 0) {
-        sm.m[warp][r0 + 8 * x] = m[x];
-        sm.l[warp][r0 + 8 * x] = l[x];
-      }
+      if ((lane & 3) == 0) sm.l[warp][r0 + 8 * x] = l[x];
     }
     tc::bar_sync(1, kWarps * 32);
-    float f[2];
+    unsigned odd = 0;                   // rows with something not finite in this warp's columns
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      float mm = kNoKey;
+      const int r = r0 + 8 * x;
+      float ll = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sm.m[w][r0 + 8 * x]);
-      f[x] = exp2f(m[x] - mm);
-    }
-    for (int w = 0; w < kWarps; ++w) {
-      if (w == warp) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (r0 + 8 * x >= rows) continue;
-            float2 *to = reinterpret_cast<float2 *>(&sm.o[r0 + 8 * x][n * 8 + c0]);
-            float2 v = make_float2(o[n][2 * x] * f[x], o[n][2 * x + 1] * f[x]);
-            if (w > 0) v.x += to->x, v.y += to->y;
-            *to = v;
-          }
-      }
-      tc::bar_sync(1, kWarps * 32);
-    }
-    constexpr int E = D / 32;
-    for (int r = warp; r < rows; r += kWarps) {
-      float mm = kNoKey, ll = 0.f, v[E];
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sm.m[w][r]);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) ll += sm.l[w][r] * exp2f(sm.m[w][r] - mm);
+      for (int w = 0; w < kWarps; ++w) ll += sm.l[w][r];
       bool fine = isfinite(ll);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        v[e] = sm.o[r][lane * E + e];
-        fine = fine && isfinite(v[e]);
-      }
-      if (!__all_sync(0xffffffffu, fine)) {
-        exact_row_write<__nv_bfloat16, D>(a, Piece(p), kKeys, r, part, kStreamRows);
-        continue;
-      }
+      for (int n = 0; n < NT; ++n) fine = fine && isfinite(o[n][2 * x]) && isfinite(o[n][2 * x + 1]);
+      const unsigned bad = __ballot_sync(0xffffffffu, r < rows && !fine);   // 4 lanes per row
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (bad >> (4 * i) & 15u) odd |= 1u << (8 * x + i);
+      if (r >= rows) continue;
       if (p.slot >= 0) {
         const size_t at = (size_t)p.slot * kStreamRows + r;
 #pragma unroll
-        for (int e = 0; e < E; ++e) part.o[at * D + lane * E + e] = v[e];
-        if (lane == 0) part.ml[at] = make_float2(mm, ll);
+        for (int n = 0; n < NT; ++n)
+          *reinterpret_cast<float2 *>(part.o + at * D + (warp * NT + n) * 8 + c0) = make_float2(o[n][2 * x], o[n][2 * x + 1]);
+        if (warp == 0 && (lane & 3) == 0) part.ml[at] = make_float2(m[x], ll);
       } else {
         const size_t at = (size_t)(p.q.t0 + p.i0 + r / a.g) * a.H + p.h * a.g + r % a.g;
         const float inv = ll == 0.f ? 0.f : 1.f / ll;
-        uint32_t *to = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(a.o) + at * D + lane * E);
 #pragma unroll
-        for (int e = 0; e < E; e += 2) to[e / 2] = tc::pack_bf16(v[e] * inv, v[e + 1] * inv);
-        if (a.lse && lane == 0) a.lse[at] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+        for (int n = 0; n < NT; ++n)
+          *reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(a.o) + at * D + (warp * NT + n) * 8 + c0) =
+              tc::pack_bf16(o[n][2 * x] * inv, o[n][2 * x + 1] * inv);
+        if (a.lse && warp == 0 && (lane & 3) == 0) a.lse[at] = ll == 0.f ? -INFINITY : (m[x] + log2f(ll)) * kLn2;
       }
     }
-    tc::bar_sync(1, kWarps * 32);       // before the next piece's maxima
+    if (lane == 0) sm.odd[warp] = odd;
+    tc::bar_sync(1, kWarps * 32);       // also: the next piece writes the maxima and sums anew
+    unsigned rows_odd = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) rows_odd |= sm.odd[w];
+    if (rows_odd) {
+      // such a row is written again, by one warp, after every warp's columns of it
+      for (int r = warp; r < rows; r += kWarps)
+        if (rows_odd >> r & 1u) exact_row_write<__nv_bfloat16, D>(a, Piece(p), kKeys, r, part, kStreamRows);
+    }
   }
+  if (threadIdx.x == 0) a.items[0][blockIdx.x] = item;
 }
 
 template <int D> cudaError_t launch(const PagedArgs &a, const PagedGeometry &g, cudaStream_t s) {

@@ -171,8 +171,10 @@ __device__ void softmax(const PagedArgs &a, TileSmem<D> &sm, const Waits &wait, 
   const Partial part{a.part_o[1], reinterpret_cast<float2 *>(a.part_ml[1])};
   const float sc = a.scale * kLog2e;
   uint32_t it = 0, ns = 0, no = 0;
+  JoinItem item{};
   for (Cursor<kKeys> cur(a, 1, 2 * tpt, blockIdx.x); cur.valid(); cur.next()) {
     const Piece &p = cur.p;
+    item = cur.join_item();
     const Half hf(a, p, tpt, x);
     if (hf.rows == 0) {
       it += 2 * (p.j1 - p.j0);
@@ -284,6 +286,7 @@ __device__ void softmax(const PagedArgs &a, TileSmem<D> &sm, const Waits &wait, 
     for (unsigned odd = __ballot_sync(0xffffffffu, live && !fine); odd; odd &= odd - 1)
       exact_row_write<__nv_bfloat16, D>(a, Piece(p), kKeys, x * tpt * a.g + wrow + __ffs(odd) - 1, part, kTileRows2);
   }
+  if (threadIdx.x == 0) a.items[1][blockIdx.x] = item;
 }
 
 template <int D>
