@@ -79,6 +79,7 @@ __device__ void produce(const PagedArgs &a, const CUtensorMap *kmap, const CUten
       if (mine)
         tc::tma_load_3d(sm.kv[st][lane / per] + half * (kKeys * 128) + x * box * 128, lane < per ? kmap : vmap,
                         &sm.full[st], half * 64, row, 0);
+      __syncwarp();                    // no lane runs ahead into the next wait, which would hold the others up
       if (mine && j + 1 < p.j1) row = box_row(a, p, range, tile_index(p.t, j + 1) * kKeys + x * box, box);
     }
   }
@@ -217,6 +218,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&sm.empty[st]);
+      __syncwarp();
     }
     // the sum over the warps' keys; the output's columns are this warp's own
 #pragma unroll

@@ -3,22 +3,35 @@
 //
 // A CTA holds two 128-row query tiles of one (sequence, key/value head): rows
 // are (token, head of the group), so 128 / g tokens per tile.  Each tile has
-// its warpgroup, which owns its rows' softmax (thread = row = TMEM lane); one
-// warp loads, one issues the products.  Per tile of 128 keys:
+// its warpgroup for its rows' softmax (thread = row = TMEM lane); one warp
+// loads, one issues the products.  Per tile of 128 keys:
 //
 //   load    K, V by TMA, a page (or 64 rows of it) per box, into a ring of
 //           tile-sized slots
 //   MMA     S_q = Q_q K^T                       (128 x 128, TMEM)
-//   rows    P_q = 2^(S scale log2 e - m) in bf16, over S_q's own columns;
-//           sums in fp32 from the unrounded weights
+//   rows    P_q = 2^(S scale log2 e - m) in bf16, over S_q's own columns,
+//           64 keys at a time; sums in fp32 from the unrounded weights
 //   MMA     O_q (+)= P_q V                      (128 x d, TMEM)
 //
 // The products of one query tile run while the other's rows are in the
-// softmax: PV_0(j), QK_0(j+1), PV_1(j), QK_1(j+1).  m is moved, and O
-// rescaled in TMEM, only when a row's maximum has grown by more than 2^8
-// since m was set: weights then stay below 2^8, well inside bf16 and fp32.
-// S_q(j+1) is issued after PV_q(j), so the barrier that announces S_q(j+1)
-// also says that O_q is complete up to j.
+// softmax: PV_0(j), QK_0(j+1), PV_1(j), QK_1(j+1), the first half of PV(j) as
+// soon as the first half of P(j) is there.  S_q(j+1) is issued after PV_q(j),
+// so the barrier that announces S_q(j+1) also says that O_q is complete up to
+// j.
+//
+// The weights of a tile are formed with the m there is, while the tile's
+// maximum is found: they need not stay below 1, since bf16 and fp32 have the
+// range.  When the maximum has passed m by 2^8, m is moved before the next
+// tile and O rescaled in TMEM.  A row whose maximum rises by more than 2^96
+// within one tile could overflow: it is computed again, exactly, at the end.
+//
+// What it took (8192 tokens of a 16K prompt, 32 heads on 8): 1.91 ms with a
+// maximum before the weights and the products issued by lane 0 (their
+// descriptors then go through vector registers, 120 cycles per product
+// instead of 64); 1.62 ms with an elected lane.  One S for both query tiles,
+// so that QK_q(j+1) need not wait for PV_q(j), gave 1.63 ms: all 128 logits
+// of a row then have to be in registers at once.  Four softmax warpgroups
+// with half a row per thread: 2.37 ms.
 //
 // Bound by the exponentials and the products about equally: 16384 weights
 // per (query tile, key tile) take 1024 cycles of the SM's 16 exp2 per cycle,
@@ -30,15 +43,15 @@ namespace paged {
 namespace {
 
 constexpr int kKeys = 128, kThreads = 320;
-constexpr uint32_t kTmemCols = 512;
-constexpr float kSlack = 8.f;                     // log2 of the largest weight before m is moved
+constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256;   // S_x (and P_x), O_x at 128 x from there
+constexpr float kSlack = 8.f, kRange = 96.f;      // log2 of the weights from which m is moved, and of the largest
 
 template <int D> constexpr uint32_t tile_bytes() { return 128 * D * 2; }
 template <int D> constexpr int slots() { return D == 128 ? 5 : 10; }
 template <int D> struct TileSmem {
   unsigned char q[2][tile_bytes<D>()];
   unsigned char kv[slots<D>()][tile_bytes<D>()];  // K, V, K, V, ...
-  uint64_t q_full, q_empty, kv_full[slots<D>()], kv_empty[slots<D>()], s_full[2], p_full[2], o_full[2];
+  uint64_t q_full, q_empty, kv_full[slots<D>()], kv_empty[slots<D>()], s_full[2], p_full[2][2], o_full[2];
   uint32_t tmem, dead;
 };
 
@@ -46,6 +59,30 @@ LZ_DEV float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
   return y;
+}
+// One lane of a converged warp.  The issuing branches go by this and not by
+// the lane's number: the compiler then knows that one thread is in them and
+// keeps the products' descriptors in uniform registers.
+LZ_DEV bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
+// Two fp32 operations in one instruction.
+LZ_DEV float2 fma2(float2 x, float2 y, float2 z) {
+  float2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n"
+      : "=l"(reinterpret_cast<uint64_t &>(r))
+      : "l"(reinterpret_cast<uint64_t &>(x)), "l"(reinterpret_cast<uint64_t &>(y)),
+        "l"(reinterpret_cast<uint64_t &>(z)));
+  return r;
+}
+LZ_DEV float2 add2(float2 x, float2 y) {
+  float2 r;
+  asm("add.rn.f32x2 %0, %1, %2;\n"
+      : "=l"(reinterpret_cast<uint64_t &>(r))
+      : "l"(reinterpret_cast<uint64_t &>(x)), "l"(reinterpret_cast<uint64_t &>(y)));
+  return r;
 }
 // 32 lanes x 32-bit, 32 consecutive columns per thread.
 LZ_DEV void tmem_st32(uint32_t taddr, const uint32_t *r) {
@@ -104,6 +141,7 @@ __device__ void produce(const PagedArgs &a, const CUtensorMap *qmap, const CUten
         if (mine)
           tc::tma_load_3d(sm.kv[st] + half * tc::kReg + x * box * 128, kv ? vmap : kmap, &sm.kv_full[st], half * 64,
                           row, 0);
+        __syncwarp();
       }
       if (mine && j + 1 < p.j1) row = box_row(a, p, range, tile_index(p.t, j + 1) * kKeys + x * box, box);
     }
@@ -114,60 +152,71 @@ template <int D>
 __device__ void multiply(const PagedArgs &a, TileSmem<D> &sm, const Waits &wait, uint32_t tmem, int tpt) {
   constexpr int S = slots<D>();
   constexpr uint32_t id_s = tc::idesc_bf16(128, 128, 0, 0), id_o = tc::idesc_bf16(128, D, 0, 1);
-  const int lane = threadIdx.x & 31;
   uint32_t it = 0, pieces = 0, np[2] = {0, 0};
+  // One lane issues; the others stay with it (__syncwarp): lanes that ran ahead
+  // into the next wait would keep the warp in it and hold that lane up.
   const auto qk = [&](int x, uint32_t k) {
-    if (lane != 0 || *wait.dead) return;
-    const uint32_t q = tc::smem_u32(sm.q[x]), kk = tc::smem_u32(sm.kv[k % S]);
+    if (elect_one()) {
+      const uint32_t q = tc::smem_u32(sm.q[x]), kk = tc::smem_u32(sm.kv[k % S]);
 #pragma unroll
-    for (int s = 0; s < D / 16; ++s)
-      tc::mma_ss(tmem + x * 128, tc::desc_k(q, s), tc::desc_k(kk, s), id_s, s > 0);
-    tc::mma_commit(&sm.s_full[x]);
+      for (int s = 0; s < D / 16; ++s)
+        tc::mma_ss(tmem + kColS + x * 128, tc::desc_k(q, s), tc::desc_k(kk, s), id_s, s > 0);
+      tc::mma_commit(&sm.s_full[x]);
+    }
+    __syncwarp();
   };
   const auto full = [&](uint32_t k) {
     wait(&sm.kv_full[k % S], (k / S) & 1);
     tc::tc_fence_after();
   };
   const auto release = [&](uint64_t *bar) {
-    if (lane == 0 && !*wait.dead) tc::mma_commit(bar);
+    if (elect_one()) tc::mma_commit(bar);
+    __syncwarp();
   };
   for (Cursor<kKeys> cur(a, 1, 2 * tpt, blockIdx.x); cur.valid(); cur.next(), ++pieces) {
     const Piece &p = cur.p;
-    const int halves = p.i0 + tpt < p.i1 ? 2 : 1;
+    const int halves = p.i0 + tpt < p.i1 ? 2 : 1, n = p.j1 - p.j0;
     wait(&sm.q_full, pieces & 1);
     full(it);
     for (int x = 0; x < halves; ++x) qk(x, it);
     release(&sm.kv_empty[it % S]);
-    if (p.j1 - p.j0 == 1) release(&sm.q_empty);
-    for (int j = p.j0; j < p.j1; ++j, it += 2) {
-      const bool more = j + 1 < p.j1;
+    if (n == 1) release(&sm.q_empty);
+    for (int j = 0; j < n; ++j, it += 2) {
+      const bool more = j + 1 < n;
       full(it + 1);
       if (more) full(it + 2);
+      const uint32_t v = tc::smem_u32(sm.kv[(it + 1) % S]);
       for (int x = 0; x < halves; ++x) {
-        wait(&sm.p_full[x], np[x]++ & 1);
-        tc::tc_fence_after();
-        if (lane == 0 && !*wait.dead) {
-          const uint32_t v = tc::smem_u32(sm.kv[(it + 1) % S]);
 #pragma unroll
-          for (int s = 0; s < kKeys / 16; ++s)
-            tc::mma_ts(tmem + 256 + x * 128, tmem + x * 128 + s * 8, tc::desc_mn(v, s), id_o, j > p.j0 || s > 0);
-          if (!more) tc::mma_commit(&sm.o_full[x]);
+        for (int h = 0; h < 2; ++h) {
+          wait(&sm.p_full[x][h], np[x] & 1);
+          tc::tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int s = 4 * h; s < 4 * h + 4; ++s)
+              tc::mma_ts(tmem + kColO + x * 128, tmem + kColS + x * 128 + s * 8, tc::desc_mn(v, s), id_o,
+                         j > 0 || s > 0);
+            if (h == 1 && !more) tc::mma_commit(&sm.o_full[x]);
+          }
+          __syncwarp();
         }
+        ++np[x];
         if (more) qk(x, it + 2);
       }
       release(&sm.kv_empty[(it + 1) % S]);
       if (more) release(&sm.kv_empty[(it + 2) % S]);
-      if (more && j + 2 == p.j1) release(&sm.q_empty);
+      if (j + 2 == n) release(&sm.q_empty);
     }
   }
 }
 
 template <int D>
 __device__ void softmax(const PagedArgs &a, TileSmem<D> &sm, const Waits &wait, uint32_t tmem, int tpt) {
-  constexpr int S = slots<D>();
-  const int lane = threadIdx.x & 31, x = threadIdx.x >> 7, wrow = (threadIdx.x >> 5 & 3) * 32, row = wrow + lane;
+  constexpr int S = slots<D>(), C = 64;       // columns at a time
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, x = warp >> 2;
+  const int wrow = (warp & 3) * 32, row = wrow + lane;
   const uint32_t lanes = (uint32_t)wrow << 16;
-  const uint32_t ts = tmem + lanes + x * 128, to = tmem + lanes + 256 + x * 128;
+  const uint32_t ts = tmem + lanes + kColS + x * 128, to = tmem + lanes + kColO + x * 128;
   const Partial part{a.part_o[1], reinterpret_cast<float2 *>(a.part_ml[1])};
   const float sc = a.scale * kLog2e;
   uint32_t it = 0, ns = 0, no = 0;
@@ -176,17 +225,23 @@ __device__ void softmax(const PagedArgs &a, TileSmem<D> &sm, const Waits &wait, 
     const Piece &p = cur.p;
     item = cur.join_item();
     const Half hf(a, p, tpt, x);
+    const int n = p.j1 - p.j0;
     if (hf.rows == 0) {
-      it += 2 * (p.j1 - p.j0);
+      it += 2 * n;
       continue;
     }
     const Range range(a, p);
     const int base = p.q.s - p.q.n, first = base + hf.first, last = first + hf.tokens - 1;
     const int pos = row < hf.rows ? first + row / a.g : -1;
-    float m = kNoKey, l = 0.f;
-    for (int j = p.j0; j < p.j1; ++j, it += 2) {
-      const int k0 = tile_index(p.t, j) * kKeys;
-      if (!range.whole(k0, kKeys)) {
+    const bool busy = wrow < hf.rows;         // some row of this warp is one of the item's
+    // tiles within [clear0, clear1) need no mask here and no zeroed values
+    const int clear0 = a.window > 0 ? last - a.window + 1 : 0, clear1 = base + p.i0 + 1;
+    int k0 = tile_index(p.t, p.j0) * kKeys;
+    float m = kNoKey, l = 0.f, top = kNoKey;  // top: the largest logit so far
+    for (int j = 0; j < n; ++j, it += 2) {
+      if (j > 0) k0 = p.j0 + j == p.t.nsink ? p.t.first * kKeys : k0 + kKeys;
+      const bool clear = k0 >= clear0 && k0 + kKeys <= clear1;
+      if (!clear && !range.whole(k0, kKeys)) {
         // values that no row sees may be anything: their weight is zero, so make them zero
         const uint32_t v = it + 1;
         wait(&sm.kv_full[v % S], (v / S) & 1);
@@ -195,31 +250,38 @@ __device__ void softmax(const PagedArgs &a, TileSmem<D> &sm, const Waits &wait, 
             *tc::chunk_ptr(sm.kv[v % S], 0, e / (D / 8), e % (D / 8)) = make_uint4(0, 0, 0, 0);
         tc::fence_proxy_async();
       }
+      const int hi = pos - k0, lo = a.window > 0 ? hi - a.window : INT_MIN, sk = a.window > 0 ? a.sinks - k0 : 0;
+      float s[C];
+      const auto load = [&](int c) {
+        tc::tmem_ld32x2(ts + c, ts + c + 32, s, s + 32);
+        if (!clear) {
+#pragma unroll
+          for (int e = 0; e < C; ++e)
+            if (!(c + e <= hi && (c + e > lo || c + e < sk))) s[e] = -INFINITY;
+        }
+      };
+      const auto raise = [&]() {              // top over these columns
+        float mx[2] = {s[0], s[1]};
+#pragma unroll
+        for (int e = 2; e < C; e += 2) mx[e >> 1 & 1] = fmaxf(fmaxf(mx[e >> 1 & 1], s[e]), s[e + 1]);
+        top = fmaxf(top, fmaxf(mx[0], mx[1]) * sc);
+      };
       wait(&sm.s_full[x], ns++ & 1);
       tc::tc_fence_after();
-      if (wrow < hf.rows) {
-        float s[128];
-        tc::tmem_ld32x2(ts, ts + 32, s, s + 32);
-        tc::tmem_ld32x2(ts + 64, ts + 96, s + 64, s + 96);
-        const bool all = k0 + kKeys - 1 <= first &&
-                         (a.window == 0 || k0 > last - a.window || k0 + kKeys - 1 < a.sinks);
-        if (!all) {
-          const int hi = pos - k0, lo = a.window > 0 ? hi - a.window : INT_MIN, sk = a.window > 0 ? a.sinks - k0 : 0;
-#pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (!(c <= hi && (c > lo || c < sk))) s[c] = -INFINITY;
+      if (busy) {
+        if (__any_sync(0xffffffffu, m == kNoKey)) {     // a row has seen no key yet
+          load(0);
+          raise();
+          load(C);
+          raise();
         }
-        float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-        for (int c = 4; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
         if (__any_sync(0xffffffffu, top > m + kSlack)) {
           const float mn = fmaxf(m, top), f = ex2(m - mn);     // f = 0 at the first key
           m = mn;
           l *= f;
-          if (j > p.j0) {
-            float o[16];                     // few at a time: the row's 128 logits stay in registers
-#pragma unroll
+          if (j > 0) {
+            float o[16];
+#pragma unroll 1
             for (int c = 0; c < D; c += 16) {
               tc::tmem_ld16(to + c, o);
 #pragma unroll
@@ -229,29 +291,39 @@ __device__ void softmax(const PagedArgs &a, TileSmem<D> &sm, const Waits &wait, 
             }
           }
         }
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int c = 0; c < 128; c += 64) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int e = 0; e < 64; e += 2) {
-            const float w0 = ex2(fmaf(s[c + e], sc, -m)), w1 = ex2(fmaf(s[c + e + 1], sc, -m));
-            sum[(e >> 1) & 3] += w0 + w1;
-            // weights go to the second product in bf16 (half a step, 2^-8 of each); the sum keeps 32 bits
-            pk[e / 2] = tc::pack_bf16(w0, w1);
-          }
-          tmem_st32(ts + c / 2, pk);
-        }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tc::tmem_st_wait();
       }
-      tc::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&sm.p_full[x]);
+      const float2 sc2 = make_float2(sc, sc), m2 = make_float2(-m, -m);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (busy) {
+          load(h * C);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          float mx[2] = {s[0], s[1]};
+          uint32_t pk[C / 2];
+#pragma unroll
+          for (int e = 0; e < C; e += 2) {
+            if (e > 0) mx[e >> 1 & 1] = fmaxf(fmaxf(mx[e >> 1 & 1], s[e]), s[e + 1]);
+            float2 w = fma2(make_float2(s[e], s[e + 1]), sc2, m2);
+            w = make_float2(ex2(w.x), ex2(w.y));
+            sum[e >> 1 & 1] = add2(sum[e >> 1 & 1], w);
+            // weights go to the second product in bf16 (half a step, 2^-8 of each); the sum keeps 32 bits
+            pk[e / 2] = tc::pack_bf16(w.x, w.y);
+          }
+          tmem_st32(ts + h * (C / 2), pk);
+          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          top = fmaxf(top, fmaxf(mx[0], mx[1]) * sc);
+          tc::tmem_st_wait();
+        }
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sm.p_full[x][h]);
+        __syncwarp();
+      }
+      if (top > m + kRange) l = NAN;
     }
     wait(&sm.o_full[x], no++ & 1);
     tc::tc_fence_after();
-    if (wrow >= hf.rows) continue;
+    if (!busy) continue;
     // out: 32 columns at a time, unnormalised sums for a split item
     const int r = x * tpt * a.g + row;
     const bool live = row < hf.rows;
@@ -294,8 +366,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     paged_tile_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ CUtensorMap qmap,
                       const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, int tpt) {
   constexpr int S = slots<D>();
-  extern __shared__ unsigned char raw[];
-  TileSmem<D> &sm = *reinterpret_cast<TileSmem<D> *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) unsigned char raw[];
+  TileSmem<D> &sm = *reinterpret_cast<TileSmem<D> *>(raw);
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     tc::mbar_init(&sm.q_full, 1);
@@ -306,7 +378,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&sm.s_full[i], 1);
-      tc::mbar_init(&sm.p_full[i], 4);
+      tc::mbar_init(&sm.p_full[i][0], 4);
+      tc::mbar_init(&sm.p_full[i][1], 4);
       tc::mbar_init(&sm.o_full[i], 1);
     }
     sm.dead = 0;
@@ -348,7 +421,8 @@ template <int D> cudaError_t launch(const PagedArgs &a, const PagedGeometry &g, 
   const int tpt = g.tok[1] / 2;
   if (!make_query_map(&qmap, a, tpt) || !make_pool_map(&kmap, a.k_pages, a) || !make_pool_map(&vmap, a.v_pages, a))
     return cudaErrorInvalidValue;
-  const size_t smem = sizeof(TileSmem<D>) + 1024;
+  const size_t smem = sizeof(TileSmem<D>);
+  static_assert(sizeof(TileSmem<D>) <= 232448, "227 KB of shared memory per CTA");
   const cudaError_t e = cudaFuncSetAttribute(paged_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)smem);
   if (e != cudaSuccess) return e;

@@ -22,6 +22,7 @@ struct Waits {
   volatile uint32_t *dead;   // shared memory, 0 at the start
   uint32_t *status;
   LZ_DEV bool operator()(uint64_t *bar, uint32_t parity) const {
+    if (tc::mbar_try_wait(bar, parity)) return true;
     if (*dead) return false;
     if (tc::mbar_wait(bar, parity, status, ST_TIMEOUT)) return true;
     *dead = 1;
