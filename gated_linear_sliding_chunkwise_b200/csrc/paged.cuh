@@ -18,6 +18,8 @@
 #include <float.h>
 #include <limits.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "lizard_internal.h"
 
@@ -34,6 +36,18 @@ constexpr float kNoKey = -FLT_MAX;   // running maximum before any key was seen
 // writes are visible.
 LZ_DEV void pdl_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 LZ_DEV void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+// Raises a kernel's shared-memory limit, once per device.
+struct SmemOnce {
+  std::atomic<bool> done[64] = {};
+  cudaError_t operator()(const void *kernel, size_t smem) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && done[dev].load(std::memory_order_acquire))) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess && dev < 64) done[dev].store(true, std::memory_order_release);
+    return e;
+  }
+};
 template <typename... P, typename... A>
 cudaError_t pdl_launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
   cudaLaunchAttribute at{};

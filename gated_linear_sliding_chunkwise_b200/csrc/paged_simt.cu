@@ -192,8 +192,8 @@ __global__ void __launch_bounds__(256, 2) paged_simt_kernel(PagedArgs a, int tok
 template <typename T, int D>
 cudaError_t launch(const PagedArgs &a, const PagedGeometry &g, cudaStream_t s) {
   const size_t smem = sizeof(SimtSmem<D>);
-  const cudaError_t e = cudaFuncSetAttribute(paged_simt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)smem);
+  static SmemOnce once;
+  const cudaError_t e = once(reinterpret_cast<const void *>(paged_simt_kernel<T, D>), smem);
   if (e != cudaSuccess) return e;
   return pdl_launch(paged_simt_kernel<T, D>, g.ctas[1], 256, smem, s, a, g.tok[1]);
 }

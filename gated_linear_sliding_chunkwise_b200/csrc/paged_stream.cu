@@ -277,8 +277,8 @@ template <int D> cudaError_t launch(const PagedArgs &a, const PagedGeometry &g, 
   CUtensorMap kmap, vmap;
   if (!make_pool_map(&kmap, a.k_pages, a) || !make_pool_map(&vmap, a.v_pages, a)) return cudaErrorInvalidValue;
   const size_t smem = sizeof(StreamSmem<D>) + 1024;
-  const cudaError_t e = cudaFuncSetAttribute(paged_stream_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)smem);
+  static SmemOnce once;
+  const cudaError_t e = once(reinterpret_cast<const void *>(paged_stream_kernel<D>), smem);
   if (e != cudaSuccess) return e;
   return pdl_launch(paged_stream_kernel<D>, g.ctas[0], kThreads, smem, s, a, kmap, vmap);
 }

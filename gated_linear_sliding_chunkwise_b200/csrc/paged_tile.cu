@@ -423,8 +423,8 @@ template <int D> cudaError_t launch(const PagedArgs &a, const PagedGeometry &g, 
     return cudaErrorInvalidValue;
   const size_t smem = sizeof(TileSmem<D>);
   static_assert(sizeof(TileSmem<D>) <= 232448, "227 KB of shared memory per CTA");
-  const cudaError_t e = cudaFuncSetAttribute(paged_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)smem);
+  static SmemOnce once;
+  const cudaError_t e = once(reinterpret_cast<const void *>(paged_tile_kernel<D>), smem);
   if (e != cudaSuccess) return e;
   return pdl_launch(paged_tile_kernel<D>, g.ctas[1], kThreads, smem, s, a, qmap, kmap, vmap, tpt);
 }
