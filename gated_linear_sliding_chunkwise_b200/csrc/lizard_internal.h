@@ -311,6 +311,7 @@ constexpr int kSMs = 148;                       // SMs of a B200
 constexpr int kSimtCtas = 2 * kSMs, kStreamCtas = 2 * kSMs, kTileCtas = kSMs;
 constexpr int kStreamRows = 16, kTileRows2 = 256, kSimtRows = 64;   // rows of an item
 constexpr int kMaxGroup = 64;                   // query heads per key/value head
+constexpr int kAlone = 256;                     // sequences up to which the streaming kernel needs no prep
 }  // namespace paged
 
 struct PagedArgs {
@@ -326,6 +327,7 @@ struct PagedArgs {
   long long *prefix;             // [2][B + 1]
   paged::Seq *seqs;              // [B]
   paged::JoinItem *items[2];     // [CTAs of the class]
+  uint32_t *found;               // [CTAs of class 0]: status bits, where there is no prep
   // partial sums per class: [slots][rows][d] fp32 and [slots][rows] (maximum, sum)
   float *part_o[2];
   float *part_ml[2];
@@ -338,6 +340,7 @@ struct PagedGeometry {
   int kt[2], tok[2], ctas[2];    // keys per tile, tokens per item, CTAs (0: class not launched)
   int least[2];                  // fewest tiles a CTA takes
   int slot_rows[2];              // rows of a partial slot
+  bool alone;                    // class 0 only, with no prep: the streaming kernel does its work
 };
 cudaError_t launch_paged_prep(const PagedArgs &a, const PagedGeometry &g, bool bf16, cudaStream_t s);
 cudaError_t launch_paged_simt(const PagedArgs &a, const PagedGeometry &g, bool bf16, cudaStream_t s);

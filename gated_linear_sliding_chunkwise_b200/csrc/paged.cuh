@@ -116,22 +116,36 @@ LZ_DEV bool sees(const PagedArgs &a, int p, int j) {
 
 // Page that holds tokens [pg * page, ...) of a row; -1 (and the status bit)
 // when the table's entry is outside the pool.
-LZ_DEV int page_id(const PagedArgs &a, int row, int pg) {
+LZ_DEV int page_id(const PagedArgs &a, uint32_t *status, int row, int pg) {
   int id = -1;
   if (pg < a.max_pages) id = a.table[(size_t)row * a.max_pages + pg];
   if ((unsigned)id >= (unsigned)a.num_pages) {
-    atomicOr(a.status, ST_INDEX);
+    atomicOr(status, ST_INDEX);
     id = -1;
   }
   return id;
 }
 
 // --------------------------------------------------------------- split ----
-// Written by the prep kernel for each class of sequences (class 0: few rows,
-// class 1: the others): prefix[b] = tiles of the sequences before b.
+// For each class of sequences (class 0: few rows, class 1: the others).
 struct Split {
   long long total, share;
 };
+// The work of a class: prefix[b] = tiles of the sequences before b.  Written
+// by the prep kernel, or found by each CTA for itself (streaming kernel).
+struct Work {
+  const long long *prefix;
+  const Seq *seqs;
+  Split split;
+};
+LZ_DEV Work planned(const PagedArgs &a, int cls) {
+  return Work{a.prefix + (size_t)cls * (a.B + 1), a.seqs, a.split[cls]};
+}
+// A CTA's share of `total` tiles over n CTAs.
+LZ_DEV long long share_of(long long total, int n, int least) {
+  const long long share = total < INT_MAX ? ((int)total + n - 1) / n : (total + n - 1) / n;
+  return share > least ? share : least;
+}
 struct Piece {
   int b, h, item;        // sequence, key/value head, item within (b, h)
   int i0, i1;            // its tokens
@@ -156,6 +170,7 @@ template <int KT>
 struct Cursor {
   const PagedArgs &a;
   const long long *prefix;
+  const Seq *seqs;
   int tok;               // tokens per item
   long long u, end, share;
   int cta;
@@ -164,13 +179,13 @@ struct Cursor {
   // Latency counts here: every CTA starts with it.  The search for the
   // sequence probes 32 places at a time (one step for 32 sequences, two for
   // 1024), and its first probes do not wait for the split.
-  LZ_DEV Cursor(const PagedArgs &a_, int cls, int tok_, int cta_) : a(a_), tok(tok_), cta(cta_) {
+  LZ_DEV Cursor(const PagedArgs &a_, const Work &work, int tok_, int cta_)
+      : a(a_), prefix(work.prefix), seqs(work.seqs), tok(tok_), cta(cta_) {
     const int lane = threadIdx.x & 31;
-    prefix = a.prefix + (size_t)cls * (a.B + 1);
     int lo = 0, width = a.B;                      // the sequence is one of lo .. lo + width - 1
     int step = (width + 31) / 32;
     long long probe = prefix[min(lane * step, a.B)];
-    const Split sp = a.split[cls];
+    const Split sp = work.split;
     share = sp.share;
     u = share * cta;
     end = min(u + share, sp.total);
@@ -257,7 +272,7 @@ struct Cursor {
 
  private:
   LZ_DEV void open_seq() {
-    p.q = a.seqs[p.b];
+    p.q = seqs[p.b];
     nitem = (p.q.n + tok - 1) / tok;
   }
   LZ_DEV void open_item(int j0) {
@@ -284,8 +299,8 @@ struct Partial {
 // NaN; a row whose result is not finite is computed again here.  One warp;
 // lane l gets elements l * D / 32 ...
 template <typename T, int D>
-__device__ __noinline__ void exact_row(const PagedArgs &a, const Piece &p, int KT, int r, float *acc, float &m_out,
-                                       float &l_out) {
+__device__ __noinline__ void exact_row(const PagedArgs &a, uint32_t *status, const Piece &p, int KT, int r, float *acc,
+                                       float &m_out, float &l_out) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
   const int tok = p.i0 + r / a.g, head = p.h * a.g + r % a.g;
@@ -300,7 +315,7 @@ __device__ __noinline__ void exact_row(const PagedArgs &a, const Piece &p, int K
     const int k0 = tile_index(p.t, jt) * KT;
     for (int j = k0; j < k0 + KT && j <= pos; ++j) {
       if (!sees(a, pos, j)) continue;
-      const int id = page_id(a, p.q.row, j / a.page);
+      const int id = page_id(a, status, p.q.row, j / a.page);
       if (id < 0) continue;
       const size_t at = (((size_t)id * a.Hkv + p.h) * a.page + j % a.page) * D + lane * E;
       const T *k = static_cast<const T *>(a.k_pages) + at;
@@ -323,12 +338,12 @@ __device__ __noinline__ void exact_row(const PagedArgs &a, const Piece &p, int K
 
 // Recomputes a row and writes it where it belongs: the partial slot, or o and lse.
 template <typename T, int D>
-__device__ __noinline__ void exact_row_write(const PagedArgs &a, const Piece &p, int KT, int r, const Partial &part,
-                                             int slot_rows) {
+__device__ __noinline__ void exact_row_write(const PagedArgs &a, uint32_t *status, const Piece &p, int KT, int r,
+                                             const Partial &part, int slot_rows) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
   float acc[E], m, l;
-  exact_row<T, D>(a, p, KT, r, acc, m, l);
+  exact_row<T, D>(a, status, p, KT, r, acc, m, l);
   if (p.slot >= 0) {
     const size_t at = (size_t)p.slot * slot_rows + r;
 #pragma unroll

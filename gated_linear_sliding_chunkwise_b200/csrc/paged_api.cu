@@ -77,12 +77,14 @@ lz::PagedGeometry choose(const lizard_paged_args *a) {
   if ((long long)a->max_q * g > c.few) {
     c.ctas[1] = lz::paged::kTileCtas;
     c.slot_rows[1] = lz::paged::kTileRows2;
+  } else {
+    c.alone = a->B <= lz::paged::kAlone;
   }
   return c;
 }
 
 struct PagedLayout {
-  size_t split, prefix, seqs, items[2], part_o[2], part_ml[2], total;
+  size_t split, prefix, seqs, found, items[2], part_o[2], part_ml[2], total;
 };
 PagedLayout paged_layout(const lizard_paged_args *a, const lz::PagedGeometry &c) {
   PagedLayout l{};
@@ -90,6 +92,7 @@ PagedLayout paged_layout(const lizard_paged_args *a, const lz::PagedGeometry &c)
   l.split = off; off += up(2 * 2 * sizeof(long long));
   l.prefix = off; off += up(2 * ((size_t)a->B + 1) * sizeof(long long));
   l.seqs = off; off += up((size_t)a->B * 4 * sizeof(int));
+  l.found = off; off += up((size_t)c.ctas[0] * sizeof(uint32_t));
   for (int x = 0; x < 2; ++x) {
     l.items[x] = off; off += up((size_t)c.ctas[x] * 4 * sizeof(int));
     const size_t rows = 2 * (size_t)c.ctas[x] * c.slot_rows[x];
@@ -144,12 +147,13 @@ lizard_status lizard_paged_attn(const lizard_paged_args *a, lizard_stream_t stre
   p.split = at<lz::paged::Split>(ws, lay.split);
   p.prefix = at<long long>(ws, lay.prefix);
   p.seqs = at<lz::paged::Seq>(ws, lay.seqs);
+  p.found = at<uint32_t>(ws, lay.found);
   for (int x = 0; x < 2; ++x) {
     p.items[x] = at<lz::paged::JoinItem>(ws, lay.items[x]);
     p.part_o[x] = at<float>(ws, lay.part_o[x]);
     p.part_ml[x] = at<float>(ws, lay.part_ml[x]);
   }
-  if (lz::launch_paged_prep(p, c, bf16, s) != cudaSuccess) return LIZARD_ERR_CUDA;
+  if (!c.alone && lz::launch_paged_prep(p, c, bf16, s) != cudaSuccess) return LIZARD_ERR_CUDA;
   if (c.ctas[0] && lz::launch_paged_stream(p, c, s) != cudaSuccess) return LIZARD_ERR_CUDA;
   if (c.ctas[1] &&
       (on_tensor_cores(a) ? lz::launch_paged_tile(p, c, s) : lz::launch_paged_simt(p, c, bf16, s)) != cudaSuccess)

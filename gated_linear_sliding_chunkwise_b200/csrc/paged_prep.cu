@@ -83,8 +83,7 @@ __device__ void split_batch(const PagedArgs &a, const PagedGeometry &g) {
     for (int c = 0; c < 2; ++c) {
       a.prefix[(size_t)c * (a.B + 1) + a.B] = base[c];
       a.split[c].total = base[c];
-      const long long n = g.ctas[c] > 0 ? g.ctas[c] : 1, share = (base[c] + n - 1) / n;
-      a.split[c].share = share > g.least[c] ? share : g.least[c];
+      a.split[c].share = share_of(base[c], g.ctas[c] > 0 ? g.ctas[c] : 1, g.least[c]);
     }
   }
 }
@@ -163,6 +162,12 @@ __device__ void join(const PagedArgs &a, const PagedGeometry &g, int cls) {
 template <typename T, int D>
 __global__ void __launch_bounds__(256) paged_join_kernel(PagedArgs a, PagedGeometry g) {
   pdl_wait();
+  if (g.alone && blockIdx.x == 0 && blockIdx.y == 0) {   // the CTAs' findings make the call's status
+    uint32_t st = 0;
+    for (int c = threadIdx.x; c < g.ctas[0]; c += 256) st |= a.found[c];
+    const int index = __syncthreads_or(st & ST_INDEX), timeout = __syncthreads_or(st & ST_TIMEOUT);
+    if (threadIdx.x == 0) *a.status = (index ? ST_INDEX : 0u) | (timeout ? ST_TIMEOUT : 0u);
+  }
   const int cls = g.ctas[0] ? blockIdx.z : 1;
   if ((int)blockIdx.x + 1 < g.ctas[cls]) join<T, D>(a, g, cls);
 }

@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(256, 2) paged_simt_kernel(PagedArgs a, int tok
   const Partial part{a.part_o[1], reinterpret_cast<float2 *>(a.part_ml[1])};
   const float sc = a.scale * kLog2e;
   JoinItem item{};
-  for (Cursor<kKeys> cur(a, 1, tok, blockIdx.x); cur.valid(); cur.next()) {
+  for (Cursor<kKeys> cur(a, planned(a, 1), tok, blockIdx.x); cur.valid(); cur.next()) {
     const Piece &p = cur.p;
     item = cur.join_item();
     const int rows = (p.i1 - p.i0) * a.g, base = p.q.s - p.q.n;
@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(256, 2) paged_simt_kernel(PagedArgs a, int tok
       __syncthreads();                      // the last tile's reads
       if (tid < kKeys) {
         const int j = k0 + tid;
-        sm.page[tid] = j < end && (j >= low || j < a.sinks) ? page_id(a, p.q.row, j / a.page) : -1;
+        sm.page[tid] = j < end && (j >= low || j < a.sinks) ? page_id(a, a.status, p.q.row, j / a.page) : -1;
       }
       __syncthreads();
       for (int x = tid; x < kKeys * D / 4; x += 256) {
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(256, 2) paged_simt_kernel(PagedArgs a, int tok
       const unsigned odd = __ballot_sync(0xffffffffu, r < rows && !fine);
       for (int half = 0; half < 2; ++half)
         if (odd & (0xffffu << (16 * half)))
-          exact_row_write<T, D>(a, Piece(p), kKeys, ((tid >> 5) * 2 + half) * 4 + i, part, kRows);
+          exact_row_write<T, D>(a, a.status, Piece(p), kKeys, ((tid >> 5) * 2 + half) * 4 + i, part, kRows);
     }
   }
   if (tid == 0) a.items[1][blockIdx.x] = item;

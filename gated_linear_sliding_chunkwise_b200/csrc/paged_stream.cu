@@ -14,6 +14,12 @@
 // in shared memory (two barriers of 128 threads a tile): no warp holds another
 // sum for the same output, so a piece ends without a join of the warps, which
 // took 4.6 us of a call with one token.
+//
+// A call that only has such sequences, at most kAlone of them, needs no kernel
+// before this one (ALONE): each CTA checks the batch and splits the work for
+// itself in shared memory, and the CTA that holds a new token's tile puts its
+// key and value into the page and into the tile it has just loaded (no other
+// CTA reads that head's rows there).  One token at 517 keys: 13.7 -> 11.2 us.
 #include "paged_tma.cuh"
 
 namespace lz {
@@ -29,8 +35,10 @@ template <int D> struct StreamSmem {
   unsigned char p[kStreamRows * 128];                  // weights, bf16 [row][key], 128-byte swizzle
   float m[kWarps][kStreamRows], l[kWarps][kStreamRows];
   uint32_t odd[kWarps];
+  long long prefix[kAlone + 1], warp_sums[kWarps + 1];   // the work, where there is no prep
+  Seq seqs[kAlone];
   uint64_t full[stages<D>()], empty[stages<D>()];
-  uint32_t dead;
+  uint32_t dead, found;
 };
 
 LZ_DEV uint32_t kv_offset(int row, int chunk) {   // 16-byte chunk of a row
@@ -56,20 +64,57 @@ LZ_DEV void mma16816(float *c, const uint32_t *a, uint32_t b0, uint32_t b1) {
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The batch's checks and the prefix of its tiles, by the whole CTA.
+template <int D> LZ_DEV Work find_work(const PagedArgs &a, StreamSmem<D> &sm, int least) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long total = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+    const int b = b0 + threadIdx.x;
+    long long tiles = 0;
+    if (b < a.B) {
+      bool bad;
+      const Seq q = check_seq(a, b, &bad);
+      if (bad) atomicOr(&sm.found, ST_INDEX);
+      sm.seqs[b] = q;
+      if (q.n > 0) tiles = (long long)tiles_of<kKeys>(a, q, 0, q.n).count * a.Hkv;
+    }
+    long long x = tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) sm.warp_sums[warp] = x;
+    __syncthreads();
+    long long before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w <= kWarps; ++w) {
+      if (w < warp) before += sm.warp_sums[w];
+      all += sm.warp_sums[w];
+    }
+    if (b < a.B) sm.prefix[b] = total + before + x - tiles;
+    total += all;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) sm.prefix[a.B] = total;
+  __syncthreads();
+  return Work{sm.prefix, sm.seqs, Split{total, share_of(total, gridDim.x, least)}};
+}
+
 template <int D>
-__device__ void produce(const PagedArgs &a, const CUtensorMap *kmap, const CUtensorMap *vmap, StreamSmem<D> &sm,
-                        const Waits &wait) {
+__device__ void produce(const PagedArgs &a, const Work &work, const CUtensorMap *kmap, const CUtensorMap *vmap,
+                        StreamSmem<D> &sm, const Waits &wait) {
   constexpr int S = stages<D>();
   const int lane = threadIdx.x & 31;
   const int box = min(a.page, 64), boxes = kKeys / box, per = boxes * (D / 64);
   int it = 0;
-  for (Cursor<kKeys> cur(a, 0, kStreamRows, blockIdx.x); cur.valid(); cur.next()) {
+  for (Cursor<kKeys> cur(a, work, kStreamRows, blockIdx.x); cur.valid(); cur.next()) {
     const Piece &p = cur.p;
     const Range range(a, p);
     // lane i < 2 per loads box x of half `half` of K (i < per) or V
     const int x = lane % per % boxes, half = lane % per / boxes;
     const bool mine = lane < 2 * per;
-    int row = mine ? box_row(a, p, range, tile_index(p.t, p.j0) * kKeys + x * box, box) : 0;
+    int row = mine ? box_row(a, wait.status, p, range, tile_index(p.t, p.j0) * kKeys + x * box, box) : 0;
     for (int j = p.j0; j < p.j1; ++j, ++it) {
       const int st = it % S;
       if (it >= S) wait(&sm.empty[st], (it / S - 1) & 1);
@@ -80,41 +125,21 @@ __device__ void produce(const PagedArgs &a, const CUtensorMap *kmap, const CUten
         tc::tma_load_3d(sm.kv[st][lane / per] + half * (kKeys * 128) + x * box * 128, lane < per ? kmap : vmap,
                         &sm.full[st], half * 64, row, 0);
       __syncwarp();                    // no lane runs ahead into the next wait, which would hold the others up
-      if (mine && j + 1 < p.j1) row = box_row(a, p, range, tile_index(p.t, j + 1) * kKeys + x * box, box);
+      if (mine && j + 1 < p.j1) row = box_row(a, wait.status, p, range, tile_index(p.t, j + 1) * kKeys + x * box, box);
     }
   }
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 2)
-    paged_stream_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ CUtensorMap kmap,
-                        const __grid_constant__ CUtensorMap vmap) {
+template <int D, bool ALONE>
+__device__ void consume(const PagedArgs &a, const Work &work, StreamSmem<D> &sm, const Waits &wait) {
   constexpr int S = stages<D>(), KS = D / 16, NT = D / 8 / kWarps;   // NT: 8-column blocks of this warp
-  extern __shared__ unsigned char raw[];
-  StreamSmem<D> &sm = *reinterpret_cast<StreamSmem<D> *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < S; ++i) {
-      tc::mbar_init(&sm.full[i], 1);
-      tc::mbar_init(&sm.empty[i], kWarps);
-    }
-    sm.dead = 0;
-    tc::fence_barrier_init();
-  }
-  __syncthreads();
-  pdl_wait();
-  pdl_trigger();
-  const Waits wait{&sm.dead, a.status};
-  if (warp == kWarps) {
-    produce<D>(a, &kmap, &vmap, sm, wait);
-    return;
-  }
   const Partial part{a.part_o[0], reinterpret_cast<float2 *>(a.part_ml[0])};
   const float sc = a.scale * kLog2e;
   const int r0 = lane >> 2, c0 = (lane & 3) * 2;       // fragment rows r0, r0 + 8; columns c0, c0 + 1
   int it = 0;
   JoinItem item{};
-  for (Cursor<kKeys> cur(a, 0, kStreamRows, blockIdx.x); cur.valid(); cur.next()) {
+  for (Cursor<kKeys> cur(a, work, kStreamRows, blockIdx.x); cur.valid(); cur.next()) {
     const Piece &p = cur.p;
     item = cur.join_item();
     const Range range(a, p);
@@ -151,6 +176,25 @@ __global__ void __launch_bounds__(kThreads, 2)
             *reinterpret_cast<uint4 *>(sm.kv[st][1] + kv_offset(warp * 16 + x / (D / 8), x % (D / 8))) =
                 make_uint4(0, 0, 0, 0);
         tc::fence_proxy_async();       // before the stage is loaded again
+      }
+      if (ALONE && a.k && kw + 16 > max(base, 0) && kw < p.q.s) {
+        // new tokens among this warp's keys: into their page and over what was loaded for them
+        for (int j = max(kw, max(base, 0)); j < min(kw + 16, p.q.s); ++j) {
+          constexpr int L = D / 8;               // 16-byte pieces of a row
+          const size_t from = ((size_t)(p.q.t0 + j - base) * a.Hkv + p.h) * L;
+          const int id = a.table[(size_t)p.q.row * a.max_pages + j / a.page];
+          const size_t to = (((size_t)id * a.Hkv + p.h) * a.page + j % a.page) * L;
+          const bool there = (unsigned)id < (unsigned)a.num_pages;   // the producer reports it where it is not
+          for (int x = lane; x < 2 * L; x += 32) {
+            const bool v = x >= L;
+            const int c = v ? x - L : x;
+            const uint4 u = static_cast<const uint4 *>(v ? a.v : a.k)[from + c];
+            *reinterpret_cast<uint4 *>(sm.kv[st][v] + kv_offset(j - k0, c)) = u;
+            if (there) static_cast<uint4 *>(v ? a.v_pages : a.k_pages)[to + c] = u;
+          }
+        }
+        tc::fence_proxy_async();       // before the stage is loaded again
+        __syncwarp();
       }
       float s[2][4];
 #pragma unroll
@@ -267,20 +311,55 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (rows_odd) {
       // such a row is written again, by one warp, after every warp's columns of it
       for (int r = warp; r < rows; r += kWarps)
-        if (rows_odd >> r & 1u) exact_row_write<__nv_bfloat16, D>(a, Piece(p), kKeys, r, part, kStreamRows);
+        if (rows_odd >> r & 1u) exact_row_write<__nv_bfloat16, D>(a, wait.status, Piece(p), kKeys, r, part, kStreamRows);
     }
   }
   if (threadIdx.x == 0) a.items[0][blockIdx.x] = item;
+}
+
+template <int D, bool ALONE>
+__global__ void __launch_bounds__(kThreads, 2)
+    paged_stream_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ CUtensorMap kmap,
+                        const __grid_constant__ CUtensorMap vmap, int least) {
+  constexpr int S = stages<D>();
+  extern __shared__ unsigned char raw[];
+  StreamSmem<D> &sm = *reinterpret_cast<StreamSmem<D> *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S; ++i) {
+      tc::mbar_init(&sm.full[i], 1);
+      tc::mbar_init(&sm.empty[i], kWarps);
+    }
+    sm.dead = sm.found = 0;
+    tc::fence_barrier_init();
+  }
+  __syncthreads();
+  if (!ALONE) pdl_wait();
+  pdl_trigger();
+  const Waits wait{&sm.dead, ALONE ? &sm.found : a.status};
+  const Work work = ALONE ? find_work<D>(a, sm, least) : planned(a, 0);
+  if (warp == kWarps) produce<D>(a, work, &kmap, &vmap, sm, wait);
+  else consume<D, ALONE>(a, work, sm, wait);
+  if (ALONE) {
+    __syncthreads();
+    if (threadIdx.x == 0) a.found[blockIdx.x] = sm.found;
+  }
 }
 
 template <int D> cudaError_t launch(const PagedArgs &a, const PagedGeometry &g, cudaStream_t s) {
   CUtensorMap kmap, vmap;
   if (!make_pool_map(&kmap, a.k_pages, a) || !make_pool_map(&vmap, a.v_pages, a)) return cudaErrorInvalidValue;
   const size_t smem = sizeof(StreamSmem<D>) + 1024;
-  static SmemOnce once;
-  const cudaError_t e = once(reinterpret_cast<const void *>(paged_stream_kernel<D>), smem);
+  static SmemOnce once, once_alone;
+  if (!g.alone) {
+    const cudaError_t e = once(reinterpret_cast<const void *>(paged_stream_kernel<D, false>), smem);
+    if (e != cudaSuccess) return e;
+    return pdl_launch(paged_stream_kernel<D, false>, g.ctas[0], kThreads, smem, s, a, kmap, vmap, g.least[0]);
+  }
+  const cudaError_t e = once_alone(reinterpret_cast<const void *>(paged_stream_kernel<D, true>), smem);
   if (e != cudaSuccess) return e;
-  return pdl_launch(paged_stream_kernel<D>, g.ctas[0], kThreads, smem, s, a, kmap, vmap);
+  paged_stream_kernel<D, true><<<g.ctas[0], kThreads, smem, s>>>(a, kmap, vmap, g.least[0]);
+  return cudaGetLastError();
 }
 
 }  // namespace

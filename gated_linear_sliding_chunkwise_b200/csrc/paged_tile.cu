@@ -116,7 +116,7 @@ __device__ void produce(const PagedArgs &a, const CUtensorMap *qmap, const CUten
   const int x = lane % boxes, half = lane / boxes;
   const bool mine = lane < per;
   int it = 0, pieces = 0;
-  for (Cursor<kKeys> cur(a, 1, 2 * tpt, blockIdx.x); cur.valid(); cur.next(), ++pieces) {
+  for (Cursor<kKeys> cur(a, planned(a, 1), 2 * tpt, blockIdx.x); cur.valid(); cur.next(), ++pieces) {
     const Piece &p = cur.p;
     const Range range(a, p);
     if (pieces > 0) wait(&sm.q_empty, (pieces - 1) & 1);
@@ -129,7 +129,7 @@ __device__ void produce(const PagedArgs &a, const CUtensorMap *qmap, const CUten
           tc::tma_load_3d(sm.q[h] + c * tc::kReg, qmap, &sm.q_full, c * 64, p.h * a.g, p.q.t0 + p.i0 + h * tpt);
     }
     __syncwarp();
-    int row = mine ? box_row(a, p, range, tile_index(p.t, p.j0) * kKeys + x * box, box) : 0;
+    int row = mine ? box_row(a, a.status, p, range, tile_index(p.t, p.j0) * kKeys + x * box, box) : 0;
     for (int j = p.j0; j < p.j1; ++j) {
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv, ++it) {
@@ -143,7 +143,7 @@ __device__ void produce(const PagedArgs &a, const CUtensorMap *qmap, const CUten
                           row, 0);
         __syncwarp();
       }
-      if (mine && j + 1 < p.j1) row = box_row(a, p, range, tile_index(p.t, j + 1) * kKeys + x * box, box);
+      if (mine && j + 1 < p.j1) row = box_row(a, a.status, p, range, tile_index(p.t, j + 1) * kKeys + x * box, box);
     }
   }
 }
@@ -173,7 +173,7 @@ __device__ void multiply(const PagedArgs &a, TileSmem<D> &sm, const Waits &wait,
     if (elect_one()) tc::mma_commit(bar);
     __syncwarp();
   };
-  for (Cursor<kKeys> cur(a, 1, 2 * tpt, blockIdx.x); cur.valid(); cur.next(), ++pieces) {
+  for (Cursor<kKeys> cur(a, planned(a, 1), 2 * tpt, blockIdx.x); cur.valid(); cur.next(), ++pieces) {
     const Piece &p = cur.p;
     const int halves = p.i0 + tpt < p.i1 ? 2 : 1, n = p.j1 - p.j0;
     wait(&sm.q_full, pieces & 1);
@@ -221,7 +221,7 @@ __device__ void softmax(const PagedArgs &a, TileSmem<D> &sm, const Waits &wait, 
   const float sc = a.scale * kLog2e;
   uint32_t it = 0, ns = 0, no = 0;
   JoinItem item{};
-  for (Cursor<kKeys> cur(a, 1, 2 * tpt, blockIdx.x); cur.valid(); cur.next()) {
+  for (Cursor<kKeys> cur(a, planned(a, 1), 2 * tpt, blockIdx.x); cur.valid(); cur.next()) {
     const Piece &p = cur.p;
     item = cur.join_item();
     const Half hf(a, p, tpt, x);
@@ -356,7 +356,7 @@ __device__ void softmax(const PagedArgs &a, TileSmem<D> &sm, const Waits &wait, 
     }
     tc::tc_fence_before();
     for (unsigned odd = __ballot_sync(0xffffffffu, live && !fine); odd; odd &= odd - 1)
-      exact_row_write<__nv_bfloat16, D>(a, Piece(p), kKeys, x * tpt * a.g + wrow + __ffs(odd) - 1, part, kTileRows2);
+      exact_row_write<__nv_bfloat16, D>(a, a.status, Piece(p), kKeys, x * tpt * a.g + wrow + __ffs(odd) - 1, part, kTileRows2);
   }
   if (threadIdx.x == 0) a.items[1][blockIdx.x] = item;
 }

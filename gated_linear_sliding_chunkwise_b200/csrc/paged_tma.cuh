@@ -49,10 +49,10 @@ struct Range {
 // Row of the pool's map where the box of tokens [j, j + box) begins.  Boxes
 // without a key that is seen, and pages outside the pool, lie past the map's
 // end: they read as zeros.
-LZ_DEV int box_row(const PagedArgs &a, const Piece &p, const Range &r, int j, int box) {
+LZ_DEV int box_row(const PagedArgs &a, uint32_t *status, const Piece &p, const Range &r, int j, int box) {
   const int none = a.num_pages * a.Hkv * a.page;
   if (!r.some(j, box)) return none;
-  const int id = page_id(a, p.q.row, j / a.page);
+  const int id = page_id(a, status, p.q.row, j / a.page);
   return id < 0 ? none : (id * a.Hkv + p.h) * a.page + j % a.page;
 }
 
