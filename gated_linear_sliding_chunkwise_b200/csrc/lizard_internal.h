@@ -337,7 +337,7 @@ struct PagedArgs {
 // k, v into their pages.
 struct PagedGeometry {
   int few;                       // rows up to which a sequence belongs to class 0
-  int kt[2], tok[2], ctas[2];    // keys per tile, tokens per item, CTAs (0: class not launched)
+  int kt[2], tok[2], ctas[2];    // keys per tile, tokens per item, CTAs launched (0: class not launched)
   int least[2];                  // fewest tiles a CTA takes
   int slot_rows[2];              // rows of a partial slot
   bool alone;                    // class 0 only, with no prep: the streaming kernel does its work

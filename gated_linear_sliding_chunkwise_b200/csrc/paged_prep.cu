@@ -123,18 +123,18 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(PagedArgs a, P
 }
 
 // Joins a split item's pieces: o = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i
-// over the CTAs that the item spans, in order.  Block x takes the item that
-// begins in CTA x's stretch, if one does; its rows go over blockIdx.y and the
-// warps, a lane takes D / 32 columns.
+// over the CTAs that the item spans, in order.  `parts` blocks take the item
+// that begins in CTA `first`'s stretch, if one does, and go over its rows with
+// their warps; a lane takes D / 32 columns.
 template <typename T, int D>
-__device__ void join(const PagedArgs &a, const PagedGeometry &g, int cls) {
+__device__ void join(const PagedArgs &a, const PagedGeometry &g, int cls, int first, int part, int parts) {
   constexpr int E = D / 32;
-  const int first = blockIdx.x, slot_rows = g.slot_rows[cls];
+  const int slot_rows = g.slot_rows[cls];
   const JoinItem d = a.items[cls][first];
   const int lane = threadIdx.x & 31;
   const float *po = a.part_o[cls];
   const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml[cls]);
-  for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < d.rows; r += gridDim.y * 8) {
+  for (int r = part * 8 + (threadIdx.x >> 5); r < d.rows; r += parts * 8) {
     float m = kNoKey, l = 0.f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
@@ -158,25 +158,37 @@ __device__ void join(const PagedArgs &a, const PagedGeometry &g, int cls) {
   }
 }
 
-// blockIdx.z: the class, counted from the first one that was launched.
+// Blocks of an item of a class: 16 rows each (two per warp: the join waits for
+// its loads, so more blocks beat one wave of larger ones: 64 rows each took
+// 13 us longer on prompt chunks of four users).
+LZ_DEV __host__ int join_parts(const PagedGeometry &g, int cls) { return (g.slot_rows[cls] + 15) / 16; }
+
+// First the blocks of class 0, then those of class 1.  (The
+// last CTA's stretch begins no item that goes on.)
 template <typename T, int D>
 __global__ void __launch_bounds__(256) paged_join_kernel(PagedArgs a, PagedGeometry g) {
   pdl_wait();
-  if (g.alone && blockIdx.x == 0 && blockIdx.y == 0) {   // the CTAs' findings make the call's status
+  if (g.alone && blockIdx.x == 0) {   // the CTAs' findings make the call's status
     uint32_t st = 0;
     for (int c = threadIdx.x; c < g.ctas[0]; c += 256) st |= a.found[c];
     const int index = __syncthreads_or(st & ST_INDEX), timeout = __syncthreads_or(st & ST_TIMEOUT);
     if (threadIdx.x == 0) *a.status = (index ? ST_INDEX : 0u) | (timeout ? ST_TIMEOUT : 0u);
   }
-  const int cls = g.ctas[0] ? blockIdx.z : 1;
-  if ((int)blockIdx.x + 1 < g.ctas[cls]) join<T, D>(a, g, cls);
+  int x = blockIdx.x, cls = 0;
+  const int few = max(g.ctas[0] - 1, 0) * join_parts(g, 0);
+  if (x >= few) {
+    x -= few;
+    cls = 1;
+  }
+  const int parts = join_parts(g, cls);
+  join<T, D>(a, g, cls, x / parts, x % parts, parts);
 }
 
 template <typename T, int D> cudaError_t launch_join(const PagedArgs &a, const PagedGeometry &g, cudaStream_t s) {
-  const int most = g.ctas[0] > g.ctas[1] ? g.ctas[0] : g.ctas[1];
-  const int rows = g.ctas[1] ? g.slot_rows[1] : g.slot_rows[0];
-  const dim3 grid(most - 1, (rows + 31) / 32, g.ctas[0] && g.ctas[1] ? 2 : 1);
-  return pdl_launch(paged_join_kernel<T, D>, grid, 256, 0, s, a, g);
+  int blocks = 0;
+  for (int c = 0; c < 2; ++c)
+    if (g.ctas[c] > 0) blocks += (g.ctas[c] - 1) * join_parts(g, c);
+  return pdl_launch(paged_join_kernel<T, D>, blocks, 256, 0, s, a, g);
 }
 
 }  // namespace
