@@ -63,6 +63,30 @@ cudaError_t pdl_launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
+// 2^x by the hardware unit alone (exp2f adds a rescaling for results below
+// 2^-126, which a weight may lose).
+LZ_DEV float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+// Two fp32 operations in one instruction.
+LZ_DEV float2 fma2(float2 x, float2 y, float2 z) {
+  float2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n"
+      : "=l"(reinterpret_cast<uint64_t &>(r))
+      : "l"(reinterpret_cast<uint64_t &>(x)), "l"(reinterpret_cast<uint64_t &>(y)),
+        "l"(reinterpret_cast<uint64_t &>(z)));
+  return r;
+}
+LZ_DEV float2 add2(float2 x, float2 y) {
+  float2 r;
+  asm("add.rn.f32x2 %0, %1, %2;\n"
+      : "=l"(reinterpret_cast<uint64_t &>(r))
+      : "l"(reinterpret_cast<uint64_t &>(x)), "l"(reinterpret_cast<uint64_t &>(y)));
+  return r;
+}
+
 // ------------------------------------------------------------ sequences ---
 struct __align__(16) Seq {
   int t0, n, s, row;   // first new token in q, new tokens, length with them, table row
@@ -315,9 +339,9 @@ __device__ __noinline__ void exact_row(const PagedArgs &a, uint32_t *status, con
     const int k0 = tile_index(p.t, jt) * KT;
     for (int j = k0; j < k0 + KT && j <= pos; ++j) {
       if (!sees(a, pos, j)) continue;
-      const int id = page_id(a, status, p.q.row, j / a.page);
+      const int id = page_id(a, status, p.q.row, j >> a.shift);
       if (id < 0) continue;
-      const size_t at = (((size_t)id * a.Hkv + p.h) * a.page + j % a.page) * D + lane * E;
+      const size_t at = ((((size_t)id * a.Hkv + p.h) << a.shift) + (j & (a.page - 1))) * D + lane * E;
       const T *k = static_cast<const T *>(a.k_pages) + at;
       const T *v = static_cast<const T *>(a.v_pages) + at;
       float s = 0.f;

@@ -46,6 +46,7 @@ lizard_status check_sizes(const lizard_paged_args *a) {
   return LIZARD_OK;
 }
 
+// bf16 on the tensor-core kernels.
 bool on_tensor_cores(const lizard_paged_args *a) {
   return a->dtype == LIZARD_BF16 && a->impl != LIZARD_IMPL_SIMT;
 }
@@ -136,7 +137,9 @@ lizard_status lizard_paged_attn(const lizard_paged_args *a, lizard_stream_t stre
   p.k_pages = at<void>(a->k_pages, layer); p.v_pages = at<void>(a->v_pages, layer);
   p.table = a->table; p.lens = a->lens; p.cu_q = a->cu_q; p.row = a->row;
   p.o = a->o; p.lse = a->lse;
-  p.num_pages = a->num_pages; p.Hkv = a->Hkv; p.page = a->page; p.d = a->d; p.rows = a->rows;
+  p.num_pages = a->num_pages; p.Hkv = a->Hkv; p.page = a->page; p.d = a->d;
+  while (1 << p.shift < a->page) ++p.shift;
+  p.rows = a->rows;
   p.max_pages = a->max_pages; p.B = a->B; p.T = a->T; p.H = a->H; p.g = a->H / a->Hkv;
   p.max_q = a->max_q;
   // lengths stay below 2^30: a wider window or more first tokens are all of them

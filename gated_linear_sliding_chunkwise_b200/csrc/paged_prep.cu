@@ -114,10 +114,10 @@ __global__ void __launch_bounds__(kPrepThreads) paged_prep_kernel(PagedArgs a, P
   if (i < 0 || i >= q.n) return;               // between or behind the sequences
   const int p = q.s - q.n + i;
   if (p < 0) return;
-  const int id = a.table[(size_t)q.row * a.max_pages + p / a.page];
+  const int id = a.table[(size_t)q.row * a.max_pages + (p >> a.shift)];
   if ((unsigned)id >= (unsigned)a.num_pages) return;   // the attention kernels report it
   const int h = rest / row_chunks, c = rest % row_chunks;
-  const size_t to = (((size_t)id * a.Hkv + h) * a.page + p % a.page) * row_chunks + c;
+  const size_t to = ((((size_t)id * a.Hkv + h) << a.shift) + (p & (a.page - 1))) * row_chunks + c;
   static_cast<uint4 *>(a.k_pages)[to] = static_cast<const uint4 *>(a.k)[idx];
   static_cast<uint4 *>(a.v_pages)[to] = static_cast<const uint4 *>(a.v)[idx];
 }
@@ -143,7 +143,7 @@ __device__ void join(const PagedArgs &a, const PagedGeometry &g, int cls, int fi
       const size_t at = (size_t)(x == first ? 2 * x + 1 : 2 * x) * slot_rows + r;
       const float2 v = ml[at];
       const float mn = v.x > m ? v.x : m;
-      const float fo = exp2f(m - mn), fn = exp2f(v.x - mn);
+      const float fo = ex2(m - mn), fn = ex2(v.x - mn);
       l = l * fo + v.y * fn;
 #pragma unroll
       for (int e = 0; e < E; ++e) acc[e] = acc[e] * fo + po[at * D + lane * E + e] * fn;

@@ -182,8 +182,8 @@ __device__ void consume(const PagedArgs &a, const Work &work, StreamSmem<D> &sm,
         for (int j = max(kw, max(base, 0)); j < min(kw + 16, p.q.s); ++j) {
           constexpr int L = D / 8;               // 16-byte pieces of a row
           const size_t from = ((size_t)(p.q.t0 + j - base) * a.Hkv + p.h) * L;
-          const int id = a.table[(size_t)p.q.row * a.max_pages + j / a.page];
-          const size_t to = (((size_t)id * a.Hkv + p.h) * a.page + j % a.page) * L;
+          const int id = a.table[(size_t)p.q.row * a.max_pages + (j >> a.shift)];
+          const size_t to = ((((size_t)id * a.Hkv + p.h) << a.shift) + (j & (a.page - 1))) * L;
           const bool there = (unsigned)id < (unsigned)a.num_pages;   // the producer reports it where it is not
           for (int x = lane; x < 2 * L; x += 32) {
             const bool v = x >= L;
@@ -233,14 +233,14 @@ __device__ void consume(const PagedArgs &a, const Work &work, StreamSmem<D> &sm,
         mn[x] = m[x];
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) mn[x] = fmaxf(mn[x], sm.m[w][r0 + 8 * x]);
-        const float f = exp2f(m[x] - mn[x]);
+        const float f = ex2(m[x] - mn[x]);
         m[x] = mn[x];
         l[x] *= f;
 #pragma unroll
         for (int n = 0; n < NT; ++n) o[n][2 * x] *= f, o[n][2 * x + 1] *= f;
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-          const float w0 = exp2f(s[n][2 * x] - m[x]), w1 = exp2f(s[n][2 * x + 1] - m[x]);
+          const float w0 = ex2(s[n][2 * x] - m[x]), w1 = ex2(s[n][2 * x + 1] - m[x]);
           l[x] += w0 + w1;
           // weights go to the second product in bf16 (half a step, 2^-8 of each); the sum keeps 32 bits
           *reinterpret_cast<uint32_t *>(sm.p + tc::sw128_offset(r0 + 8 * x, warp * 16 + n * 8 + c0)) =

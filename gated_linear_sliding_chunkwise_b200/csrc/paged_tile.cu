@@ -55,11 +55,6 @@ template <int D> struct TileSmem {
   uint32_t tmem, dead;
 };
 
-LZ_DEV float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
-  return y;
-}
 // One lane of a converged warp.  The issuing branches go by this and not by
 // the lane's number: the compiler then knows that one thread is in them and
 // keeps the products' descriptors in uniform registers.
@@ -67,22 +62,6 @@ LZ_DEV bool elect_one() {
   uint32_t p;
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
   return p != 0;
-}
-// Two fp32 operations in one instruction.
-LZ_DEV float2 fma2(float2 x, float2 y, float2 z) {
-  float2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;\n"
-      : "=l"(reinterpret_cast<uint64_t &>(r))
-      : "l"(reinterpret_cast<uint64_t &>(x)), "l"(reinterpret_cast<uint64_t &>(y)),
-        "l"(reinterpret_cast<uint64_t &>(z)));
-  return r;
-}
-LZ_DEV float2 add2(float2 x, float2 y) {
-  float2 r;
-  asm("add.rn.f32x2 %0, %1, %2;\n"
-      : "=l"(reinterpret_cast<uint64_t &>(r))
-      : "l"(reinterpret_cast<uint64_t &>(x)), "l"(reinterpret_cast<uint64_t &>(y)));
-  return r;
 }
 // 32 lanes x 32-bit, 32 consecutive columns per thread.
 LZ_DEV void tmem_st32(uint32_t taddr, const uint32_t *r) {

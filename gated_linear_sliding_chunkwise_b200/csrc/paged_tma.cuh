@@ -52,8 +52,8 @@ struct Range {
 LZ_DEV int box_row(const PagedArgs &a, uint32_t *status, const Piece &p, const Range &r, int j, int box) {
   const int none = a.num_pages * a.Hkv * a.page;
   if (!r.some(j, box)) return none;
-  const int id = page_id(a, status, p.q.row, j / a.page);
-  return id < 0 ? none : (id * a.Hkv + p.h) * a.page + j % a.page;
+  const int id = page_id(a, status, p.q.row, j >> a.shift);
+  return id < 0 ? none : ((id * a.Hkv + p.h) << a.shift) + (j & (a.page - 1));
 }
 
 }  // namespace paged

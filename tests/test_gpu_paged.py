@@ -92,8 +92,8 @@ def _run(paged, seqs, *, H, Hkv, d, page, dtype, window=0, sinks=0, impl=IMPL_AU
 
 
 # ---------------------------------------------------------------- attention
-IMPLS = [(FP32, IMPL_AUTO), (BF16, IMPL_SIMT), (BF16, IMPL_AUTO)]
-IDS = ["fp32", "bf16-simt", "bf16"]
+IMPLS = [(FP32, IMPL_AUTO), (FP32, IMPL_SIMT), (BF16, IMPL_SIMT), (BF16, IMPL_AUTO)]
+IDS = ["fp32", "fp32-simt", "bf16-simt", "bf16"]
 
 
 @pytest.mark.parametrize("dtype,impl", IMPLS, ids=IDS)
