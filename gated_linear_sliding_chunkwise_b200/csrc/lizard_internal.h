@@ -320,7 +320,7 @@ struct PagedArgs {
   const int *table, *lens, *cu_q, *row;
   void *o;
   float *lse;
-  int num_pages, Hkv, page, shift, d, rows, max_pages, B, T, H, g, max_q, window, sinks;   // page = 1 << shift
+  int num_pages, Hkv, page, shift, d, rows, max_pages, B, T, H, g, ginv, max_q, window, sinks;   // page = 1 << shift
   float scale;
   uint32_t *status;
   paged::Split *split;           // [2]

@@ -87,6 +87,11 @@ LZ_DEV float2 add2(float2 x, float2 y) {
   return r;
 }
 
+// Row r of an item (r < 512) is (token, head of the group): r / g and r mod g
+// by a product with ginv = floor(2^16 / g) + 1.
+LZ_DEV int token_of(const PagedArgs &a, int r) { return (r * a.ginv) >> 16; }
+LZ_DEV int head_of(const PagedArgs &a, int r) { return r - token_of(a, r) * a.g; }
+
 // ------------------------------------------------------------ sequences ---
 struct __align__(16) Seq {
   int t0, n, s, row;   // first new token in q, new tokens, length with them, table row
@@ -327,7 +332,7 @@ __device__ __noinline__ void exact_row(const PagedArgs &a, uint32_t *status, con
                                        float &m_out, float &l_out) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
-  const int tok = p.i0 + r / a.g, head = p.h * a.g + r % a.g;
+  const int tok = p.i0 + token_of(a, r), head = p.h * a.g + head_of(a, r);
   const int pos = p.q.s - p.q.n + tok;
   const T *q = static_cast<const T *>(a.q) + ((size_t)(p.q.t0 + tok) * a.H + head) * D + lane * E;
   float qv[E];
@@ -375,7 +380,7 @@ __device__ __noinline__ void exact_row_write(const PagedArgs &a, uint32_t *statu
     if (lane == 0) part.ml[at] = make_float2(m, l);
     return;
   }
-  const int tok = p.i0 + r / a.g, head = p.h * a.g + r % a.g;
+  const int tok = p.i0 + token_of(a, r), head = p.h * a.g + head_of(a, r);
   const size_t at = (size_t)(p.q.t0 + tok) * a.H + head;
   const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll

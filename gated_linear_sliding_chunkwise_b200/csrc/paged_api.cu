@@ -141,6 +141,7 @@ lizard_status lizard_paged_attn(const lizard_paged_args *a, lizard_stream_t stre
   while (1 << p.shift < a->page) ++p.shift;
   p.rows = a->rows;
   p.max_pages = a->max_pages; p.B = a->B; p.T = a->T; p.H = a->H; p.g = a->H / a->Hkv;
+  p.ginv = 65536 / p.g + 1;
   p.max_q = a->max_q;
   // lengths stay below 2^30: a wider window or more first tokens are all of them
   p.window = a->window < (1 << 30) ? a->window : 1 << 30;

@@ -149,7 +149,7 @@ __device__ void join(const PagedArgs &a, const PagedGeometry &g, int cls, int fi
       for (int e = 0; e < E; ++e) acc[e] = acc[e] * fo + po[at * D + lane * E + e] * fn;
       m = mn;
     }
-    const size_t at = (size_t)(d.token + r / a.g) * a.H + d.head + r % a.g;
+    const size_t at = (size_t)(d.token + token_of(a, r)) * a.H + d.head + head_of(a, r);
     const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
     for (int e = 0; e < E; ++e)

@@ -31,9 +31,7 @@ template <int D> struct SimtSmem {
   int page[2][kKeys];              // page of each key of a tile, -1: no row sees it
 };
 
-template <typename T> LZ_DEV float4 load4(const T *p);
-template <> LZ_DEV float4 load4<float>(const float *p) { return *reinterpret_cast<const float4 *>(p); }
-template <> LZ_DEV float4 load4<__nv_bfloat16>(const __nv_bfloat16 *p) {
+LZ_DEV float4 load4(const __nv_bfloat16 *p) {
   const uint2 u = *reinterpret_cast<const uint2 *>(p);
   const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u.x));
   const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u.y));
@@ -97,7 +95,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(PagedArgs a, in
 #pragma unroll
       for (int i = 0; i < kRows * (D / 4) / kThreads; ++i) {
         const int r = tid / (D / 4) + i * (kThreads / (D / 4));
-        put4(&sm.q[r][c], r < rows ? from + ((size_t)(r / a.g) * a.H + r % a.g) * D : from, r < rows);
+        put4(&sm.q[r][c], r < rows ? from + ((size_t)(token_of(a, r)) * a.H + head_of(a, r)) * D : from, r < rows);
       }
     }
     __syncthreads();
@@ -109,7 +107,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(PagedArgs a, in
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int r = ty * 8 + i;
-      pos[i] = r < rows ? base + p.i0 + r / a.g : -1;
+      pos[i] = r < rows ? base + p.i0 + token_of(a, r) : -1;
       m[i] = kNoKey;
       l[i] = 0.f;
 #pragma unroll
@@ -233,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(PagedArgs a, in
       for (int c = 0; c < C / 2; ++c) fine = fine && isfinite(acc[i][c].x) && isfinite(acc[i][c].y);
       if (r < rows) {
         const size_t at = p.slot >= 0 ? (size_t)p.slot * kRows + r
-                                      : (size_t)(p.q.t0 + p.i0 + r / a.g) * a.H + p.h * a.g + r % a.g;
+                                      : (size_t)(p.q.t0 + p.i0 + token_of(a, r)) * a.H + p.h * a.g + head_of(a, r);
         const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
 #pragma unroll
         for (int c = 0; c < C; c += 2) {

@@ -149,10 +149,10 @@ __device__ void consume(const PagedArgs &a, const Work &work, StreamSmem<D> &sm,
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int r = r0 + 8 * x;
-      pos[x] = r < rows ? base + p.i0 + r / a.g : -1;
+      pos[x] = r < rows ? base + p.i0 + token_of(a, r) : -1;
       const uint32_t *q = reinterpret_cast<const uint32_t *>(
           static_cast<const __nv_bfloat16 *>(a.q) +
-          ((size_t)(p.q.t0 + p.i0 + (r < rows ? r / a.g : 0)) * a.H + p.h * a.g + (r < rows ? r % a.g : 0)) * D + c0);
+          ((size_t)(p.q.t0 + p.i0 + (r < rows ? token_of(a, r) : 0)) * a.H + p.h * a.g + (r < rows ? head_of(a, r) : 0)) * D + c0);
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         qf[k][x] = r < rows ? q[k * 8] : 0u;
@@ -294,7 +294,7 @@ __device__ void consume(const PagedArgs &a, const Work &work, StreamSmem<D> &sm,
           *reinterpret_cast<float2 *>(part.o + at * D + (warp * NT + n) * 8 + c0) = make_float2(o[n][2 * x], o[n][2 * x + 1]);
         if (warp == 0 && (lane & 3) == 0) part.ml[at] = make_float2(m[x], ll);
       } else {
-        const size_t at = (size_t)(p.q.t0 + p.i0 + r / a.g) * a.H + p.h * a.g + r % a.g;
+        const size_t at = (size_t)(p.q.t0 + p.i0 + token_of(a, r)) * a.H + p.h * a.g + head_of(a, r);
         const float inv = ll == 0.f ? 0.f : 1.f / ll;
 #pragma unroll
         for (int n = 0; n < NT; ++n)

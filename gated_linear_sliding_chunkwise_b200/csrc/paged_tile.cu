@@ -47,7 +47,8 @@ constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256;   // S_x (and P_x), 
 constexpr float kSlack = 8.f, kRange = 96.f;      // log2 of the weights from which m is moved, and of the largest
 
 template <int D> constexpr uint32_t tile_bytes() { return 128 * D * 2; }
-template <int D> constexpr int slots() { return D == 128 ? 5 : 10; }
+constexpr int kSlots = 5;                         // at d = 64 a streaming CTA then fits beside this one
+template <int D> constexpr int slots() { return kSlots; }
 template <int D> struct TileSmem {
   unsigned char q[2][tile_bytes<D>()];
   unsigned char kv[slots<D>()][tile_bytes<D>()];  // K, V, K, V, ...
@@ -211,7 +212,7 @@ __device__ void softmax(const PagedArgs &a, TileSmem<D> &sm, const Waits &wait, 
     }
     const Range range(a, p);
     const int base = p.q.s - p.q.n, first = base + hf.first, last = first + hf.tokens - 1;
-    const int pos = row < hf.rows ? first + row / a.g : -1;
+    const int pos = row < hf.rows ? first + token_of(a, row) : -1;
     const bool busy = wrow < hf.rows;         // some row of this warp is one of the item's
     // tiles within [clear0, clear1) need no mask here and no zeroed values
     const int clear0 = a.window > 0 ? last - a.window + 1 : 0, clear1 = base + p.i0 + 1;
@@ -307,7 +308,7 @@ __device__ void softmax(const PagedArgs &a, TileSmem<D> &sm, const Waits &wait, 
     const int r = x * tpt * a.g + row;
     const bool live = row < hf.rows;
     const size_t at = p.slot >= 0 ? (size_t)p.slot * kTileRows2 + r
-                                  : (size_t)(p.q.t0 + p.i0 + r / a.g) * a.H + p.h * a.g + r % a.g;
+                                  : (size_t)(p.q.t0 + p.i0 + token_of(a, r)) * a.H + p.h * a.g + head_of(a, r);
     const float inv = l == 0.f ? 0.f : 1.f / l;
     bool fine = isfinite(l);
 #pragma unroll
