@@ -172,7 +172,7 @@ LZ_DEV Work planned(const PagedArgs &a, int cls) {
 }
 // A CTA's share of `total` tiles over n CTAs.
 LZ_DEV long long share_of(long long total, int n, int least) {
-  const long long share = total < INT_MAX ? ((int)total + n - 1) / n : (total + n - 1) / n;
+  const long long share = total < INT_MAX ? ((unsigned)total + n - 1u) / (unsigned)n : (total + n - 1) / n;
   return share > least ? share : least;
 }
 struct Piece {

@@ -120,6 +120,7 @@ lizard_status lizard_paged_attn(const lizard_paged_args *a, lizard_stream_t stre
   const bool some = a->T > 0 && a->B > 0;
   if (some && (!a->q || !a->k_pages || !a->v_pages || !a->table || !a->lens || !a->cu_q || !a->o || a->max_q < 1))
     return LIZARD_ERR_INVALID_ARG;
+  if (some && a->o == a->q) return LIZARD_ERR_INVALID_ARG;   // o must not overlap q
   const void *ptrs[] = {a->q, a->k, a->v, a->k_pages, a->v_pages, a->table, a->lens, a->cu_q, a->row,
                         a->o, a->lse, a->workspace};
   for (const void *p : ptrs)

@@ -163,6 +163,7 @@ __device__ void multiply(const PagedArgs &a, TileSmem<D> &sm, const Waits &wait,
     if (n == 1) release(&sm.q_empty);
     for (int j = 0; j < n; ++j, it += 2) {
       const bool more = j + 1 < n;
+      if (*wait.dead) return;                 // no products over what did not arrive
       full(it + 1);
       if (more) full(it + 2);
       const uint32_t v = tc::smem_u32(sm.kv[(it + 1) % S]);

@@ -109,17 +109,22 @@ def _code(dtype):
     return code
 
 
-def _space(nbytes, device, workspace):
+def _space(nbytes, device, workspace, stream):
     """The caller's workspace, or one from torch's allocator for this call,
     and the last two fields of the C structs (its address and bytes)."""
     if workspace is None:
         workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+        if stream is not None:     # not handed out again before that stream has done with it
+            workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
+                                    else torch.cuda.ExternalStream(int(stream), device=device))
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {device}")
     return workspace, _TAIL.pack(workspace.data_ptr(), workspace.numel() * workspace.element_size())
 
 
 def _call(fn, where, args, index, stream):
     """The C call on the cache's device (its current stream unless one is given)."""
-    if stream is None and index >= 0:
+    if stream is None:
         if index != torch.cuda.current_device():
             with torch.cuda.device(index):
                 return _check(fn(args, torch._C._cuda_getCurrentRawStream(index)), where)
@@ -163,13 +168,15 @@ def attn(q, k, v, k_pages, v_pages, table, lens, cu_q, *, max_q, row=None, layer
         _refuse(index, ("q", q, like, dtype), ("k", k, new, dtype), ("v", v, new, dtype), ("k_pages", k_pages, pool, dtype),
                 ("v_pages", v_pages, pool, dtype), ("table", table, (rows, max_pages), _I32), ("lens", lens, (rows,), _I32),
                 ("cu_q", cu_q, (B + 1,), _I32), ("row", row, (B,), _I32), ("out", out, like, dtype))
+    if index < 0:
+        raise ValueError("the cache must be on a CUDA device")
     o = torch.empty_like(q) if out is None else out
     lse = q.new_empty((T, H), dtype=torch.float32) if want_lse else None
     args = _ATTN.pack(layers, num_pages, Hkv, page, d, rows, max_pages, B, T, H, layer, max_q, window, sinks, code, impl,
                       softmax_scale, q.data_ptr(), 0 if k is None else k.data_ptr(), 0 if v is None else v.data_ptr(),
                       k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr(), lens.data_ptr(), cu_q.data_ptr(),
                       0 if row is None else row.data_ptr(), o.data_ptr(), 0 if lse is None else lse.data_ptr(), 0, 0)
-    ws, tail = _space(_attn_size(args), q.device, workspace)
+    ws, tail = _space(_attn_size(args), q.device, workspace, stream)
     _call(_attn, "lizard_paged_attn", args[:-16] + tail, index, stream)
     return {"o": o, "lse": lse, "workspace": ws}
 
@@ -201,12 +208,14 @@ def _bookkeep(name, refs, table, lens, row, src, grow, page, pool, table_out, re
                 ("lens", lens, (rows,), _I32), ("row", row, (n,), _I32), ("src", src, (n,), _I32),
                 ("grow", grow, (n,), _I32), ("table_out", table_out, (rows, max_pages), _I32),
                 ("refs_out", refs_out, (num_pages,), _I32))
+    if index < 0:
+        raise ValueError("the cache must be on a CUDA device")
     args = _PAGES.pack(layers, num_pages, Hkv, page, d, rows, max_pages, code, n, kp, vp, refs.data_ptr(),
                        table.data_ptr(), 0 if lens is None else lens.data_ptr(), 0 if row is None else row.data_ptr(),
                        0 if src is None else src.data_ptr(), 0 if grow is None else grow.data_ptr(),
                        0 if table_out is None else table_out.data_ptr(),
                        0 if refs_out is None else refs_out.data_ptr(), 0, 0)
-    ws, tail = _space(_pages_size(args), refs.device, workspace)
+    ws, tail = _space(_pages_size(args), refs.device, workspace, stream)
     _call(_pages[name], "lizard_pages_" + name, args[:-16] + tail, index, stream)
     return ws
 

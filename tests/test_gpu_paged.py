@@ -241,6 +241,80 @@ def test_wrong_offsets_rows_lengths_and_pages_are_reported(paged):
     pt.check_attention("beside a wrong one", o[:2], None, want, 64, BF16, True)
 
 
+def test_wrong_rows_and_pages_when_decoding_are_reported(paged):
+    """The same for a call of single tokens, which no preparing kernel looks over."""
+    def call(change):
+        c = pt.build([40, 33, 300], Hkv=2, d=128, page=16, dtype=BF16)
+        q, k, v, cu = _batch([(1, 40), (1, 33), (2, 300)], H=4, Hkv=2, d=128, dtype=BF16)
+        row = torch.tensor([0, 1, 2], dtype=torch.int32)
+        change(c, cu, row)
+        g = _cuda(c)
+        out = torch.full_like(q, 7.0).cuda()
+        ws = torch.full((1 << 23,), 255, dtype=torch.uint8, device="cuda")      # whatever it held before
+        paged.attn(q.cuda(), k.cuda(), v.cuda(), g["k_pages"], g["v_pages"], g["table"], g["lens"], cu.cuda(), max_q=2,
+                   row=row.cuda(), out=out, workspace=ws)
+        return workspace_status(ws), out.cpu(), q, k, v, c
+
+    for change in (lambda c, cu, row: c["table"].__setitem__((2, 5), 10 ** 6),
+                   lambda c, cu, row: c["table"].__setitem__((2, 18), -1),      # where the new tokens go
+                   lambda c, cu, row: row.__setitem__(0, -3), lambda c, cu, row: c["lens"].__setitem__(0, 10 ** 6),
+                   lambda c, cu, row: cu.__setitem__(3, 99)):
+        assert call(change)[0] == ERR_INDEX
+    assert call(lambda c, cu, row: None)[0] == OK
+    st, o, q, k, v, c = call(lambda c, cu, row: row.__setitem__(1, 3))
+    assert st == ERR_INDEX and (o[1] == 7.0).all()
+    _append(c, k, v, torch.tensor([0, 1], dtype=torch.int32))
+    want = pt.attention(q[:1], c["k_pages"][0], c["v_pages"][0], c["table"], c["lens"], torch.tensor([0, 1]))
+    pt.check_attention("beside a wrong one", o[:1], None, want, 128, BF16, True)
+
+
+@pytest.mark.parametrize("dtype,n", [(BF16, 1), (BF16, 40), (FP32, 3)], ids=["bf16-one", "bf16-chunk", "fp32"])
+def test_pools_beyond_32_bit_offsets(paged, dtype, n):
+    """Pages whose first element lies beyond 2^31 elements, in the second of two layers."""
+    Hkv, page, d = 8, 128, 128
+    per = Hkv * page * d
+    P = (1 << 31) // per // 2 + 40
+    kp = torch.empty(2, P, Hkv, page, d, dtype=dtype, device="cuda")
+    vp = torch.empty_like(kp)
+    assert P * per + (P - 5) * per > 1 << 31
+    ids = [P - 1, P - 4, P - 2]
+    gen = torch.Generator().manual_seed(4)
+    for pool in (kp, vp):
+        for p in ids:
+            pool[1, p] = torch.randn(Hkv, page, d, generator=gen).to(dtype).cuda()
+    table, lens = torch.tensor([ids], dtype=torch.int32), torch.tensor([300], dtype=torch.int32)
+    q, k, v, cu = _batch([(n, 300)], H=8, Hkv=Hkv, d=d, dtype=dtype, gap=0)
+    r = paged.attn(q.cuda(), k.cuda(), v.cuda(), kp, vp, table.cuda(), lens.cuda(), cu.cuda(), max_q=n, layer=1,
+                   want_lse=True)
+    assert workspace_status(r["workspace"]) == OK
+    small = [torch.stack([pool[1, p].cpu() for p in ids]) for pool in (kp, vp)]
+    assert torch.equal(small[0][2, :, 300 - 256 - n:300 - 256], k.transpose(0, 1))
+    want = pt.attention(q, *small, torch.arange(3, dtype=torch.int32)[None], lens, cu)
+    pt.check_attention("far pages", r["o"], r["lse"], want, d, dtype, dtype == BF16)
+
+
+def test_a_stream_of_the_callers(paged):
+    """The calls run on the stream they are given, in its order."""
+    c = pt.build([40, 70], Hkv=2, d=64, page=16, dtype=BF16)
+    q, k, v, cu = _batch([(1, 40), (20, 70)], H=4, Hkv=2, d=64, dtype=BF16)
+    g = _cuda(c)
+    dq, dk, dv, dcu = (x.cuda() for x in (q, k, v, cu))
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    outs = []
+    for stream in (s, s.cuda_stream):
+        r = paged.attn(dq, dk, dv, g["k_pages"], g["v_pages"], g["table"], g["lens"], dcu, max_q=20, stream=stream)
+        outs.append(r["o"])
+        ws = paged.free(g["refs"], g["table"], g["lens"], torch.zeros(0, dtype=torch.int32, device="cuda"), page=16,
+                        stream=stream)
+        assert workspace_status(ws, stream=s) == OK
+    s.synchronize()
+    _append(c, k, v, cu)
+    want = pt.attention(q, c["k_pages"][0], c["v_pages"][0], c["table"], c["lens"], cu)
+    for o in outs:
+        pt.check_attention("on a stream", o, None, want, 64, BF16, True)
+
+
 def test_more_new_tokens_than_announced_are_reported(paged):
     c = _cuda(pt.build([40, 40], Hkv=1, d=64, page=16, dtype=BF16))
     q, k, v, cu = _batch([(2, 40), (3, 40)], H=1, Hkv=1, d=64, dtype=BF16)
@@ -403,6 +477,29 @@ def test_beams_trade_places(paged):
         m.fork([1, 2, 0, 1], [0, 1, 2, 3])
         assert workspace_status(paged.fork(s["k"], s["v"], *args, _ints([1, 2, 0, 1]), _ints([0, 1, 2, 3]))) == OK
         _same(m, s)
+
+
+@pytest.mark.parametrize("layers", [1, 8])
+def test_branches_of_one_source_copy_its_last_page(paged, layers):
+    """Few and many bytes (the latter share their loads): runs of one source,
+    the same source again later, a source without a part-filled page."""
+    page, Hkv, d, P, MP = 128, 8, 128, 24, 3
+    gen = torch.Generator(device="cuda").manual_seed(layers)
+    kp = torch.randn(layers, P, Hkv, page, d, generator=gen, device="cuda")
+    vp = torch.randn(layers, P, Hkv, page, d, generator=gen, device="cuda")
+    s = dict(refs=torch.zeros(P, dtype=torch.int32).cuda(), lens=torch.zeros(13, dtype=torch.int32).cuda(),
+             table=torch.full((13, MP), -1, dtype=torch.int32).cuda())
+    args = (s["refs"], s["table"], s["lens"])
+    m = pt.Model(*(x.cpu() for x in args), page)
+    m.reserve([0, 1, 2, 3], [5, 300, 256, 130])
+    paged.reserve(*args, _ints([0, 1, 2, 3]), _ints([5, 300, 256, 130]), page=page)
+    before = kp.clone(), vp.clone()
+    src, row = [0, 0, 1, 0, 2, 0, 3, 3, 1], [4, 5, 6, 7, 8, 9, 10, 11, 12]
+    m.fork(src, row)
+    assert workspace_status(paged.fork(kp, vp, *args, _ints(src), _ints(row))) == OK
+    _same(m, s)
+    where = torch.tensor(m.contents).cuda()
+    assert torch.equal(kp, before[0][:, where]) and torch.equal(vp, before[1][:, where])
 
 
 def test_empty_lists_and_pools(paged):

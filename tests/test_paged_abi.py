@@ -50,8 +50,9 @@ def _attn(paged, lz, **over):
     a = paged.PagedArgs()
     a.layers, a.num_pages, a.Hkv, a.page, a.d, a.rows, a.max_pages = 2, 10, 2, 16, 64, 4, 8
     a.B, a.T, a.H, a.layer, a.max_q, a.dtype, a.impl = 3, 7, 4, 1, 3, lz.BF16, lz.IMPL_AUTO
-    for n in ("q", "k", "v", "k_pages", "v_pages", "table", "lens", "cu_q", "row", "o", "lse", "workspace"):
+    for n in ("q", "k", "v", "k_pages", "v_pages", "table", "lens", "cu_q", "row", "lse", "workspace"):
         setattr(a, n, FAKE)
+    a.o = 2 * FAKE
     a.workspace_bytes = 1 << 40
     for n, x in over.items():
         setattr(a, n, x)
@@ -69,7 +70,7 @@ def _attn(paged, lz, **over):
     ({"softmax_scale": -1.0}, 1), ({"softmax_scale": float("nan")}, 1), ({"softmax_scale": float("inf")}, 1),
     ({"k": None}, 1), ({"v": None}, 1), ({"q": None}, 1), ({"o": None}, 1), ({"table": None}, 1), ({"lens": None}, 1),
     ({"cu_q": None}, 1), ({"k_pages": None}, 1), ({"v_pages": None}, 1), ({"q": FAKE + 8}, 1), ({"row": FAKE + 4}, 1),
-    ({"workspace": FAKE + 8}, 1), ({"workspace": None}, 5), ({"workspace_bytes": 100}, 5),
+    ({"o": FAKE}, 1), ({"workspace": FAKE + 8}, 1), ({"workspace": None}, 5), ({"workspace_bytes": 100}, 5),
 ])
 def test_attention_refuses_bad_arguments_on_host(paged, lz, over, code):
     assert lz.lib().lizard_paged_attn(ctypes.byref(_attn(paged, lz, **over)), None) == code
@@ -137,6 +138,8 @@ def test_binding_refuses_tensors_that_do_not_fit(paged):
             paged.attn(**{**good, name: bad}, max_q=2)
     with pytest.raises(ValueError):
         paged.attn(**good, max_q=2, row=i(0))
+    with pytest.raises(ValueError, match="CUDA"):            # nothing on the host reaches a kernel
+        paged.attn(**good, max_q=2)
     with pytest.raises(TypeError):
         paged.attn(**{**good, "q": q.half(), "k": k.half(), "v": k.half(), "k_pages": kp.half(), "v_pages": kp.half()},
                    max_q=2)
@@ -146,6 +149,7 @@ def test_binding_refuses_tensors_that_do_not_fit(paged):
                  lambda: paged.free(refs, table, i(3), i(0), page=16),
                  lambda: paged.fork(kp, kp, refs[:3], table, lens, i(0), i(1)),
                  lambda: paged.fork(kp, kp, refs, table, lens, i(0, 1), i(1)),
-                 lambda: paged.compact(kp, kp, refs, table, table_out=table[:1])):
+                 lambda: paged.compact(kp, kp, refs, table, table_out=table[:1]),
+                 lambda: paged.free(refs, table, lens, i(0), page=16)):
         with pytest.raises(ValueError):
             call()
