@@ -58,7 +58,11 @@ bool on_tensor_cores(const lizard_paged_args *a) {
 lz::PagedGeometry choose(const lizard_paged_args *a) {
   lz::PagedGeometry c{};
   const int g = a->H / a->Hkv;
-  c.least[0] = c.least[1] = 2;
+  // Fewest tiles worth a CTA of their own, against the join of one more piece:
+  // one token over 9 tiles takes 11.0 us with one as with two; 3 fp32 chunks
+  // of 20 tokens 18.5 us with one, 25.9 with two (class 1).
+  c.least[0] = 2;
+  c.least[1] = 1;
   if (!on_tensor_cores(a)) {
     c.kt[0] = c.kt[1] = 64;
     c.tok[0] = c.tok[1] = lz::paged::kSimtRows / g;
