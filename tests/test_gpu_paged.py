@@ -636,3 +636,41 @@ def test_a_captured_step_follows_the_lengths(paged):
                 assert torch.equal(y, z)
         for ws in graphs[w][5]:
             assert workspace_status(ws) == OK
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+def test_a_captured_mixed_batch_follows_lengths_and_offsets(paged, dtype):
+    """Decoding tokens and a chunk in one captured call (every kernel of the
+    attention): replays read the lengths, offsets and tables of the moment."""
+    H, Hkv, d, page = 8, 2, 64, 16
+    most = 600
+    c = pt.build([most] * 3, Hkv=Hkv, d=d, page=page, dtype=dtype)
+    q, k, v, cu = _batch([(1, most), (70, most), (2, most)], H=H, Hkv=Hkv, d=d, dtype=dtype, gap=0)
+    g = _cuda(c)
+    dq, dk, dv, dcu = (x.cuda() for x in (q, k, v, cu))
+    out = torch.zeros_like(dq)
+
+    def call(ws=None):
+        return paged.attn(dq, dk, dv, g["k_pages"], g["v_pages"], g["table"], g["lens"], dcu, max_q=73, window=200,
+                          sinks=5, out=out, workspace=ws)["workspace"]
+
+    ws = torch.empty_like(call())
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(ws)
+    for lens, at in (([600, 600, 600], [0, 1, 71, 73]), ([17, 71, 2], [0, 1, 71, 73]), ([599, 80, 333], [0, 73, 73, 73]),
+                     ([300, 1, 64], [0, 0, 1, 73]), ([4, 500, 90], [0, 1, 2, 3])):
+        c["lens"] = torch.tensor(lens, dtype=torch.int32)
+        cu = torch.tensor(at, dtype=torch.int32)
+        c["k_pages"], c["v_pages"] = g["k_pages"].cpu(), g["v_pages"].cpu()
+        g["lens"].copy_(c["lens"])
+        dcu.copy_(cu)
+        out.fill_(7.0)
+        for _ in range(2):
+            graph.replay()
+        assert workspace_status(ws) == OK
+        _append(c, k, v, cu)
+        want = pt.attention(q, c["k_pages"][0], c["v_pages"][0], c["table"], c["lens"], cu, window=200, sinks=5)
+        pt.check_attention(f"replayed {lens} {at}", out, None, want, d, dtype, dtype == BF16)
+        assert (out[at[-1]:] == 7.0).all()
