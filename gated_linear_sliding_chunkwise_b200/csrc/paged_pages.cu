@@ -138,10 +138,11 @@ LZ_DEV bool entries_ok(const PagesArgs &a, const int *entries, int held) {
   return __all_sync(0xffffffffu, ok);
 }
 
-// CTA 0: offsets of the list's needs (exclusive prefix); the total goes to
-// count[kMost].  A total past 2^31 cannot be: it is at most n * max_pages,
-// which is kept below 2^31.
-LZ_DEV void scan_needs(const PagesArgs &a, int *sums) {
+// Offsets of the list's needs (exclusive prefix) and their sum.  Every CTA
+// finds them for itself and writes the same values: one barrier of the call
+// less than with one CTA for all.  A sum past 2^31 cannot be: it is at most
+// n * max_pages, which is kept below 2^31.
+LZ_DEV int scan_needs(const PagesArgs &a, int *sums) {
   int base = 0;
   for (int i0 = 0; i0 < a.n; i0 += kThreads) {
     const int i = i0 + threadIdx.x;
@@ -150,7 +151,8 @@ LZ_DEV void scan_needs(const PagesArgs &a, int *sums) {
     if (i < a.n) a.offset[i] = base + off;
     base += total;
   }
-  if (threadIdx.x == 0) a.count[kMost] = base;
+  __syncthreads();
+  return base;
 }
 
 // Free pages before this CTA's segment and in the whole pool.
@@ -187,12 +189,10 @@ template <int N> __global__ void __launch_bounds__(kThreads) pages_reserve_kerne
     a.need[i] = need;
   }
   book_sync<N>();
-  if (c == 0) scan_needs(a, sums);
-  book_sync<N>();
   if (status_of(a)) return;
+  const int total = scan_needs(a, sums);
   int before, all;
   free_before<N>(a, c, before, all);
-  const int total = a.count[kMost];
   if (total > all) {
     if (c == 0 && tid == 0) report(a, ST_PAGES);
     return;
@@ -287,24 +287,16 @@ template <int N> __global__ void __launch_bounds__(kThreads) pages_fork_kernel(P
     }
   }
   book_sync<N>();
-  if (c == 0) {
-    __shared__ int copies;
-    scan_needs(a, sums);
-    __syncthreads();
-    if (tid == 0) {
-      // the copies of a call that is refused are none
-      copies = a.count[kMost];
-      int before, all;
-      free_before<N>(a, 0, before, all);
-      if (copies > all) report(a, ST_PAGES);
-      if (status_of(a)) a.count[kMost] = 0;
-    }
-  }
-  book_sync<N>();
   if (status_of(a)) return;
+  const int total = scan_needs(a, sums);
   int before, all;
   free_before<N>(a, c, before, all);
-  each_bit(g, sums, before, a.count[kMost], free_word, [&](int r, int p) { a.list[r] = p; });
+  if (total > all) {
+    if (c == 0 && tid == 0) report(a, ST_PAGES);
+    return;
+  }
+  if (c == 0 && tid == 0) a.count[kMost] = total;   // the copies to make; none of a call that is refused
+  each_bit(g, sums, before, total, free_word, [&](int r, int p) { a.list[r] = p; });
   // the shared pages' new holders, and what the replaced rows held
   for (int i = w0; i < a.n; i += N * kWarps) {
     const int r = a.row[i];
