@@ -3,7 +3,8 @@
     python -m gated_linear_sliding_chunkwise_b200.build [--force] [-v]
 
 Each ``csrc/*.cu`` is compiled to an object under ``_build/`` (skipped when
-newer than its sources), then linked into ``liblizard.so`` next to this file.
+newer than its sources), then linked into ``liblizard.so`` next to this file;
+``csrc/paged_binding.cpp`` becomes the extension module ``_paged_call.so``.
 """
 
 from __future__ import annotations
@@ -21,6 +22,7 @@ ROOT = os.path.dirname(HERE)
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "liblizard.so")
+BINDING = os.path.join(HERE, "_paged_call.so")   # Python entry of the paged cache
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -79,7 +81,31 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode:
             raise RuntimeError("link failed:\n" + r.stdout + r.stderr)
+    build_binding(force)
     return LIB
+
+
+def build_binding(force: bool = False) -> str:
+    """The extension module of the paged cache: torch's headers, linked to
+    liblizard.so beside it."""
+    src = os.path.join(CSRC, "paged_binding.cpp")
+    if not force and not _stale(BINDING, [src, os.path.join(INCLUDE, "lizard.h")]):
+        return BINDING
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension as ext
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    include = [*ext.include_paths(), sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-I{d}" for d in include), src, "-o", BINDING, f"-L{HERE}", "-llizard", f"-L{libs}", "-ltorch_python",
+           "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{libs}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode:
+        raise RuntimeError("building the binding failed:\n" + r.stdout + r.stderr)
+    return BINDING
 
 
 def main(argv=None):
