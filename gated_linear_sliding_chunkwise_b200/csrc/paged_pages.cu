@@ -8,7 +8,7 @@
 // are read once, coalesced, into a bit per page in shared memory (CTA c keeps
 // the c-th part of the pool); ranks among the free pages are population counts
 // and a block scan over those words.  It is bound by that chain of latencies,
-// not by bytes: loops over a row's pages keep four loads under way per lane.
+// not by bytes: loops over a row's pages keep kAhead loads under way per lane.
 // Page contents move in a second launch over the whole GPU, which reads the
 // list of copies that the first one made: bound by HBM.
 #include "paged.cuh"
@@ -19,6 +19,7 @@ namespace {
 
 constexpr int kMost = 8, kThreads = 1024, kWarps = kThreads / 32;   // kMost: CTAs of a cluster
 constexpr uint32_t ST_PAGES = 8u;
+constexpr int kAhead = 8;   // entries of a row under way per lane
 
 template <int N> LZ_DEV int cluster_rank() {
   if (N == 1) return 0;
@@ -126,14 +127,14 @@ template <int N> LZ_DEV void clear_marks(const PagesArgs &a, int c) {
 // The entries of a row's pages are live pages of the pool; one warp.
 LZ_DEV bool entries_ok(const PagesArgs &a, const int *entries, int held) {
   bool ok = true;
-  for (int j0 = threadIdx.x & 31; j0 < held; j0 += 128) {
-    int p[4], r[4];
+  for (int j0 = threadIdx.x & 31; j0 < held; j0 += 32 * kAhead) {
+    int p[kAhead], r[kAhead];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = j0 + 32 * i < held ? entries[j0 + 32 * i] : entries[j0];
+    for (int i = 0; i < kAhead; ++i) p[i] = j0 + 32 * i < held ? entries[j0 + 32 * i] : entries[j0];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = p[i] >= 0 && p[i] < a.num_pages ? a.refs[p[i]] : 0;
+    for (int i = 0; i < kAhead; ++i) r[i] = p[i] >= 0 && p[i] < a.num_pages ? a.refs[p[i]] : 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) ok = ok && r[i] > 0;
+    for (int i = 0; i < kAhead; ++i) ok = ok && r[i] > 0;
   }
   return __all_sync(0xffffffffu, ok);
 }
@@ -165,7 +166,7 @@ template <int N> LZ_DEV void free_before(const PagesArgs &a, int c, int &before,
   }
 }
 
-template <int N> __global__ void __launch_bounds__(kThreads) pages_reserve_kernel(PagesArgs a) {
+template <int N> __global__ void __launch_bounds__(kThreads, 1) pages_reserve_kernel(PagesArgs a) {
   extern __shared__ uint32_t bits[];
   __shared__ int sums[32];
   const int c = cluster_rank<N>(), tid = threadIdx.x, lane = tid & 31;
@@ -201,12 +202,12 @@ template <int N> __global__ void __launch_bounds__(kThreads) pages_reserve_kerne
   book_sync<N>();
   for (int i = c * kWarps + (tid >> 5); i < a.n; i += N * kWarps) {
     const int r = a.row[i], old = a.lens[r], had = pages_of(a, old), need = a.need[i], off = a.offset[i];
-    for (int j0 = lane; j0 < need; j0 += 128) {
-      int p[4];
+    for (int j0 = lane; j0 < need; j0 += 32 * kAhead) {
+      int p[kAhead];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) p[x] = j0 + 32 * x < need ? a.list[off + j0 + 32 * x] : -1;
+      for (int x = 0; x < kAhead; ++x) p[x] = j0 + 32 * x < need ? a.list[off + j0 + 32 * x] : -1;
 #pragma unroll
-      for (int x = 0; x < 4; ++x)
+      for (int x = 0; x < kAhead; ++x)
         if (p[x] >= 0) {
           a.table[(size_t)r * a.max_pages + had + j0 + 32 * x] = p[x];
           a.refs[p[x]] = 1;
@@ -217,7 +218,7 @@ template <int N> __global__ void __launch_bounds__(kThreads) pages_reserve_kerne
   }
 }
 
-template <int N> __global__ void __launch_bounds__(kThreads) pages_free_kernel(PagesArgs a) {
+template <int N> __global__ void __launch_bounds__(kThreads, 1) pages_free_kernel(PagesArgs a) {
   const int c = cluster_rank<N>(), lane = threadIdx.x & 31;
   const int w0 = c * kWarps + (threadIdx.x >> 5);
   clear_marks<N>(a, c);
@@ -233,12 +234,12 @@ template <int N> __global__ void __launch_bounds__(kThreads) pages_free_kernel(P
   for (int i = w0; i < a.n; i += N * kWarps) {
     const int r = a.row[i], held = pages_of(a, a.lens[r]);
     int *entries = a.table + (size_t)r * a.max_pages;
-    for (int j0 = lane; j0 < a.max_pages; j0 += 128) {
-      int p[4];
+    for (int j0 = lane; j0 < a.max_pages; j0 += 32 * kAhead) {
+      int p[kAhead];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) p[x] = j0 + 32 * x < held ? entries[j0 + 32 * x] : -1;
+      for (int x = 0; x < kAhead; ++x) p[x] = j0 + 32 * x < held ? entries[j0 + 32 * x] : -1;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
+      for (int x = 0; x < kAhead; ++x) {
         if (p[x] >= 0) atomicSub(a.refs + p[x], 1);
         if (j0 + 32 * x < a.max_pages) entries[j0 + 32 * x] = -1;
       }
@@ -250,7 +251,7 @@ template <int N> __global__ void __launch_bounds__(kThreads) pages_free_kernel(P
 
 // need[i]: 1 when the source's last page is part-filled; held[i]: length of
 // the source as it was; snap: its table row as it was.
-template <int N> __global__ void __launch_bounds__(kThreads) pages_fork_kernel(PagesArgs a) {
+template <int N> __global__ void __launch_bounds__(kThreads, 1) pages_fork_kernel(PagesArgs a) {
   extern __shared__ uint32_t bits[];
   __shared__ int sums[32];
   const int c = cluster_rank<N>(), tid = threadIdx.x, lane = tid & 31;
@@ -331,7 +332,7 @@ template <int N> __global__ void __launch_bounds__(kThreads) pages_fork_kernel(P
 
 // list: new number of every live page; from / to: the pages that move;
 // held: the moved pages' counts.
-template <int N> __global__ void __launch_bounds__(kThreads) pages_compact_kernel(PagesArgs a) {
+template <int N> __global__ void __launch_bounds__(kThreads, 1) pages_compact_kernel(PagesArgs a) {
   extern __shared__ uint32_t bits[];
   __shared__ int sums[32];
   const int c = cluster_rank<N>(), tid = threadIdx.x;
