@@ -28,14 +28,20 @@
 // What it took (8192 tokens of a 16K prompt, 32 heads on 8): 1.91 ms with a
 // maximum before the weights and the products issued by lane 0 (their
 // descriptors then go through vector registers, 120 cycles per product
-// instead of 64); 1.62 ms with an elected lane.  One S for both query tiles,
-// so that QK_q(j+1) need not wait for PV_q(j), gave 1.63 ms: all 128 logits
-// of a row then have to be in registers at once.  Four softmax warpgroups
-// with half a row per thread: 2.37 ms.
+// instead of 64); 1.62 ms with an elected lane; 1.57 ms as it is now, 1.05
+// PFLOP/s.  Tried and left out: one S for both query tiles, so that QK_q(j+1)
+// need not wait for PV_q(j) (1.63 ms: all 128 logits of a row then have to be
+// in registers at once); sixteen softmax warps (1.55 ms, but a mixed batch 20%
+// slower); an issuing warp for each query tile (1.70 ms: the two tiles'
+// products interleave and both softmaxes wait); exp2 on the FMA pipe for a
+// part of the weights (slower at any share).
 //
-// Bound by the exponentials and the products about equally: 16384 weights
-// per (query tile, key tile) take 1024 cycles of the SM's 16 exp2 per cycle,
-// the two products 1024 cycles of the tensor pipe at d = 128.
+// Bound by the chain softmax -> PV -> QK -> softmax of a query tile, which the
+// other tile covers only in part: per 128 keys 3.65 K cycles, of which 1.6 K
+// form the weights (16384 of them take at least 1024 cycles of the exp2 unit),
+// 1.1 K wait for the products (at least 1024 cycles at d = 128; QK reads 128
+// bytes of shared memory per cycle, all there is) and 0.9 K go into barriers,
+// loads from TMEM and the tile's bookkeeping.
 #include "paged_tma.cuh"
 
 namespace lz {
@@ -47,8 +53,7 @@ constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256;   // S_x (and P_x), 
 constexpr float kSlack = 8.f, kRange = 96.f;      // log2 of the weights from which m is moved, and of the largest
 
 template <int D> constexpr uint32_t tile_bytes() { return 128 * D * 2; }
-constexpr int kSlots = 5;                         // at d = 64 a streaming CTA then fits beside this one
-template <int D> constexpr int slots() { return kSlots; }
+template <int D> constexpr int slots() { return 5; }   // two and a half tiles of K and V (10 at d = 64: no faster)
 template <int D> struct TileSmem {
   unsigned char q[2][tile_bytes<D>()];
   unsigned char kv[slots<D>()][tile_bytes<D>()];  // K, V, K, V, ...
