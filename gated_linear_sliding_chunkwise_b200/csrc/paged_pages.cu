@@ -33,7 +33,12 @@ template <int N> LZ_DEV void book_sync() {
   else asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
 LZ_DEV void report(const PagesArgs &a, uint32_t bit) { atomicOr(a.status, bit); }
-LZ_DEV uint32_t status_of(const PagesArgs &a) { return *reinterpret_cast<volatile uint32_t *>(a.status); }
+// Whether the list was refused.  Asked after the barrier behind its checks:
+// only ST_INDEX is settled there.  ST_PAGES is recorded later, by one thread
+// and with no barrier behind it, while threads of other CTAs may still ask
+// here: they must not see it, or a CTA would go on without some of its warps.
+// (Each CTA compares the sums for itself, so all agree without the bit.)
+LZ_DEV bool list_refused(const PagesArgs &a) { return *reinterpret_cast<volatile uint32_t *>(a.status) & ST_INDEX; }
 
 // Exclusive prefix of v over the block's threads, and the block's sum.
 LZ_DEV int block_scan(int v, int *sums, int &total) {
@@ -200,7 +205,7 @@ template <int N> __global__ void __launch_bounds__(kThreads, 1) pages_reserve_ke
     a.need[i] = need;
   }
   book_sync<N>();
-  if (status_of(a)) return;
+  if (list_refused(a)) return;
   const int total = scan_needs(a, sums);
   int before, all;
   free_before<N>(a, c, before, all);
@@ -240,7 +245,7 @@ template <int N> __global__ void __launch_bounds__(kThreads, 1) pages_free_kerne
     if (lane == 0 && !(ok && first_mark(a, r))) report(a, ST_INDEX);
   }
   book_sync<N>();
-  if (status_of(a)) return;
+  if (list_refused(a)) return;
   for (int i = w0; i < a.n; i += N * kWarps) {
     const int r = a.row[i], held = pages_of(a, a.lens[r]);
     int *entries = a.table + (size_t)r * a.max_pages;
@@ -298,7 +303,7 @@ template <int N> __global__ void __launch_bounds__(kThreads, 1) pages_fork_kerne
     }
   }
   book_sync<N>();
-  if (status_of(a)) return;
+  if (list_refused(a)) return;
   const int total = scan_needs(a, sums);
   int before, all;
   free_before<N>(a, c, before, all);
