@@ -65,32 +65,32 @@ int32_t number(PyObject *o, const char *name) {
   return (int32_t)v;
 }
 
-// The call's device, made current, and its stream: the device's current one
-// unless a handle is given.
+// The call's device and stream, both made current: the device's current stream
+// unless a handle is given.  So what is allocated for the call comes from the
+// memory of the stream that it runs on: a block of the current stream may
+// still be in use there, and would go back there while the other stream works.
 struct Place {
   c10::cuda::CUDAGuard guard;
+  c10::cuda::OptionalCUDAStreamGuard on;
   c10::cuda::CUDAStream stream;
-  bool given;
   Place(at::Device device, PyObject *handle)
-      : guard(device), stream(c10::cuda::getCurrentCUDAStream(device.index())), given(handle != Py_None) {
-    if (!given) return;
+      : guard(device), stream(c10::cuda::getCurrentCUDAStream(device.index())) {
+    if (handle == Py_None) return;
     const unsigned long long h = PyLong_AsUnsignedLongLong(handle);
     if (PyErr_Occurred()) throw python_error();
     stream = c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(h), device.index());
+    on.reset_stream(stream);
   }
   lizard_stream_t handle() const { return reinterpret_cast<lizard_stream_t>(stream.stream()); }
 };
-// The caller's workspace, or one from torch's allocator, which is not handed
-// out again before the call's stream has done with it.
-Tensor space(const Tensor *given, size_t bytes, at::Device device, const Place &place) {
+// The caller's workspace, or one from torch's allocator.
+Tensor space(const Tensor *given, size_t bytes, at::Device device) {
   if (given) {
     if (given->device() != device || !given->is_contiguous())
       refuse("workspace must be contiguous and on " + device.str());
     return *given;
   }
-  Tensor t = at::empty({(int64_t)(bytes > 256 ? bytes : 256)}, at::TensorOptions().dtype(at::kByte).device(device));
-  if (place.given) t.record_stream(place.stream);
-  return t;
+  return at::empty({(int64_t)(bytes > 256 ? bytes : 256)}, at::TensorOptions().dtype(at::kByte).device(device));
 }
 void cuda_only(at::Device device) {
   if (!device.is_cuda()) refuse("the cache must be on a CUDA device");
@@ -158,7 +158,7 @@ PyObject *attn(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const Place place(device, a[18]);
     const Tensor o = out ? *out : at::empty({T, H, d}, q->options()),
                  lse = want_lse ? at::empty({T, H}, q->options().dtype(at::kFloat)) : Tensor();
-    const Tensor ws = space(given, lizard_paged_attn_workspace_size(&c), device, place);
+    const Tensor ws = space(given, lizard_paged_attn_workspace_size(&c), device);
     c.q = ptr(q); c.k = ptr(k); c.v = ptr(v); c.k_pages = ptr(kp); c.v_pages = ptr(vp);
     c.table = ints(table); c.lens = ints(lens); c.cu_q = ints(cu); c.row = ints(row);
     c.o = ptr(&o);
@@ -221,7 +221,7 @@ PyObject *bookkeep(PyObject *, PyObject *const *a, Py_ssize_t n) {
       c.refs_out = ints(&ro);
     }
     c.num_pages = P; c.rows = rows; c.max_pages = table->size(1); c.n = count;
-    const Tensor ws = space(given, lizard_pages_workspace_size(&c), device, place);
+    const Tensor ws = space(given, lizard_pages_workspace_size(&c), device);
     c.refs = ints(refs); c.table = ints(table); c.lens = ints(lens);
     c.row = ints(row); c.src = ints(src); c.grow = ints(grow);
     c.workspace = ws.data_ptr();

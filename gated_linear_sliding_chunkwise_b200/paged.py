@@ -10,6 +10,11 @@ end, ``compact`` when the pool is to shrink.
 
 Every call returns (or, for ``attn``, includes) its workspace;
 ``lizard.workspace_status(workspace)`` reads the call's device status.
+
+A call runs on ``stream`` (a torch stream or a handle), or on the current one.
+What it allocates, outputs and workspace, belongs to that stream, as it does
+under ``torch.cuda.stream(stream)``: to use it on another stream, order the two
+and call ``record_stream``.
 """
 
 from __future__ import annotations

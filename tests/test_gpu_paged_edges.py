@@ -44,3 +44,71 @@ def test_too_few_pages_for_a_long_list_change_nothing(paged):
     assert (lens == 1).all() and (refs > 0).all()
     assert torch.equal(table[half:, 0].sort().values[:-1], _ints(range(half, rows - 1)))
     assert int(table[half:, 0].max()) == P - 1
+
+
+# ------------------------------------------------------------------ streams
+def _calls(paged):
+    """Each entry point as a call that takes a stream and gives its tensors."""
+    c = _cuda(pt.build([40, 70], Hkv=2, d=64, page=16, dtype=BF16))
+    q, k, v, cu = (x.cuda() for x in _batch([(1, 40), (20, 70)], H=4, Hkv=2, d=64, dtype=BF16))
+    book, none, one, zero = (c["refs"], c["table"], c["lens"]), _ints([]), _ints([1]), _ints([0])
+
+    def attn(stream):
+        r = paged.attn(q, k, v, c["k_pages"], c["v_pages"], c["table"], c["lens"], cu, max_q=20, want_lse=True,
+                       stream=stream)
+        return [r["o"], r["lse"], r["workspace"]]
+
+    return dict(attn=attn,
+                reserve=lambda stream: [paged.reserve(*book, zero, zero, page=16, stream=stream)],
+                free=lambda stream: [paged.free(*book, none, page=16, stream=stream)],
+                fork=lambda stream: [paged.fork(c["k_pages"], c["v_pages"], *book, one, one, stream=stream)],
+                compact=lambda stream: list(paged.compact(c["k_pages"], c["v_pages"], c["refs"], c["table"],
+                                                          stream=stream)))
+
+
+def _spans(tensors):
+    return [(t.data_ptr(), t.data_ptr() + t.nbytes) for t in tensors]
+
+
+def _overlap(x, y):
+    return [(a, b) for a in x for b in y if a[0] < b[1] and b[0] < a[1]]
+
+
+@pytest.mark.parametrize("name", ["attn", "reserve", "free", "fork", "compact"])
+@pytest.mark.parametrize("handle", [False, True], ids=["stream", "handle"])
+def test_outputs_and_workspaces_belong_to_the_stream_of_the_call(paged, name, handle):
+    """No block of the current stream's memory, where work may still be pending
+    on it, is given to a call on another stream, and none of that call's goes
+    back to the current stream while the other one runs."""
+    call = _calls(paged)[name]
+    s = torch.cuda.Stream()
+    on = s.cuda_stream if handle else s
+    torch.cuda.synchronize()
+    sizes = [t.nbytes for t in call(None)]
+    torch.cuda.synchronize()
+
+    def blocks():                              # the sizes that the call wants, from the current stream's memory
+        return [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(3)]
+
+    freed = _spans(blocks())                   # recycled at once
+    out = call(on)
+    assert not _overlap(freed, _spans(out))
+    gone = _spans(out)
+    del out                                    # dropped while the stream may be at work
+    assert not _overlap(gone, _spans(blocks()))
+    with torch.cuda.stream(s):                 # they went back to the stream's own memory
+        assert _overlap(gone, _spans(blocks()))
+    torch.cuda.synchronize()
+
+
+def test_a_call_on_another_stream_leaves_the_current_stream_alone(paged):
+    torch.cuda.synchronize()
+    call, s, here = _calls(paged)["attn"], torch.cuda.Stream(), torch.cuda.current_stream()
+    torch.cuda.synchronize()
+    want = call(None)
+    torch.cuda.synchronize()
+    got = call(s)
+    assert torch.cuda.current_stream() == here
+    s.synchronize()
+    for x, y in zip(want[:2], got[:2]):
+        assert torch.equal(x[:21], y[:21])     # the rows of the sequences
