@@ -2,14 +2,15 @@
 
 Argument marshalling only: every step of the layer runs in the library's
 CUDA kernels.  PyTorch supplies device memory (outputs and workspaces are
-allocated here with torch) and the current CUDA stream.  Importing this
-module loads the library and raises ``ImportError`` if it is missing; there
-is no fallback.
+allocated here with torch, in the memory of the stream that the call runs on)
+and the current CUDA stream.  Importing this module loads the library and
+raises ``ImportError`` if it is missing; there is no fallback.
 """
 
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -173,6 +174,22 @@ def _stream(stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _on_its_stream(call):
+    """Makes the stream that a call is given current for the call, so that what
+    it allocates (and fills) belongs to that stream: a block of the current
+    stream's memory may still be in use there, and would go back there while
+    the other stream works."""
+    @functools.wraps(call)
+    def wrapper(*args, stream=None, **kwargs):
+        if stream is None:
+            return call(*args, **kwargs)
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+        with torch.cuda.stream(stream):
+            return call(*args, stream=stream, **kwargs)
+    return wrapper
+
+
 def _check(code: int, where: str):
     if code != OK:
         raise LizardError(code, where)
@@ -267,6 +284,7 @@ def make_events(n):
 
 
 # ----------------------------------------------------------------- API ----
+@_on_its_stream
 def attn_fwd(q, k, v, g, *, window, chunk=64, gate_temp=16.0, softmax_scale=0.0,
              fmap_wq=None, fmap_wk=None, meta_k=None, meta_v=None, alpha=None,
              state_in=None, want_state=False, want_lse=False,
@@ -336,6 +354,7 @@ def _bwd_struct(f, q, k, v, g, dout, *, meta_k, meta_v, fmap_wq, fmap_wk, impl, 
     return b, res
 
 
+@_on_its_stream
 def attn_bwd(q, k, v, g, dout, *, window, chunk=64, gate_temp=16.0, softmax_scale=0.0,
              fmap_wq=None, fmap_wk=None, meta_k=None, meta_v=None, alpha=None,
              state_in=None, branch=BRANCH_BOTH, impl=IMPL_AUTO, want_dstate=True,
@@ -377,6 +396,7 @@ def attn_bwd(q, k, v, g, dout, *, window, chunk=64, gate_temp=16.0, softmax_scal
     return res
 
 
+@_on_its_stream
 def stage1_step(q, k, v, g, target, *, window, chunk=64, gate_temp=16.0, softmax_scale=0.0,
                 fmap_wq=None, fmap_wk=None, meta_k=None, meta_v=None, alpha=None,
                 state_in=None, branch=BRANCH_BOTH, impl=IMPL_AUTO, want_o=False,
@@ -409,6 +429,7 @@ def stage1_step(q, k, v, g, target, *, window, chunk=64, gate_temp=16.0, softmax
     return res
 
 
+@_on_its_stream
 def decode_step(q, k, v, g, state, k_cache, v_cache, pos, *, gate_temp=16.0,
                 softmax_scale=0.0, fmap_wq=None, fmap_wk=None, meta_k=None,
                 meta_v=None, alpha=None, out=None, stream=None):
@@ -463,6 +484,7 @@ def prefill_cache(k, v, k_cache, v_cache, pos, stream=None):
 
 
 # ------------------------------------------------- sequence parallelism ---
+@_on_its_stream
 def segment_state(k, v, g, *, window, chunk=64, gate_temp=16.0, fmap_wk=None, impl=IMPL_AUTO,
                   workspace=None, stream=None):
     """(U, R) of one segment (lizard_segment_state): U [B, H, dk, dv] fp32 the
@@ -483,6 +505,7 @@ def segment_state(k, v, g, *, window, chunk=64, gate_temp=16.0, fmap_wk=None, im
     return U, R, ws
 
 
+@_on_its_stream
 def chain_states(seg_state, seg_log_decay, rank, *, state_in=None, out=None, stream=None):
     """Start state of segment `rank` (lizard_chain_states) from the gathered
     summaries seg_state [nseg, B, H, dk, dv] and seg_log_decay [nseg, B, H, dk]."""
