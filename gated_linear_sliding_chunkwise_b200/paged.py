@@ -8,8 +8,8 @@ and lens [rows] (int32).  A serving loop calls ``reserve`` for the tokens to
 come, ``attn`` once per layer, ``fork`` and ``free`` as sequences branch and
 end, ``compact`` when the pool is to shrink.
 
-Every call returns (or, for ``attn``, includes) its workspace;
-``lizard.workspace_status(workspace)`` reads the call's device status.
+Every call returns its workspace, or a result that includes it (``attn``,
+``compact``); ``lizard.workspace_status(workspace)`` reads the call's device status.
 
 A call runs on ``stream`` (a torch stream or a handle), or on the current one.
 What it allocates, outputs and workspace, belongs to that stream, as it does
@@ -112,9 +112,19 @@ def fork(k_pages, v_pages, refs, table, lens, src, row, *, workspace=None, strea
                      _handle(stream))[2]
 
 
+class Compacted(tuple):
+    """(table, refs) with the new numbers, and the call's `workspace`."""
+    workspace = None
+
+
 def compact(k_pages, v_pages, refs, table, *, table_out=None, refs_out=None, workspace=None, stream=None):
     """The live pages move to the lowest numbers (lizard_pages_compact).
     Returns (table, refs) with the new numbers: table_out and refs_out, which
-    may be table and refs themselves, or new tensors."""
-    return _bookkeep(3, refs, table, None, None, None, None, 0, k_pages, v_pages, table_out, refs_out, workspace,
-                     _handle(stream))[:2]
+    may be table and refs themselves, or new tensors.  The result's attribute
+    `workspace` holds the call's status (an entry of the table that is not a
+    live page)."""
+    table, refs, ws = _bookkeep(3, refs, table, None, None, None, None, 0, k_pages, v_pages, table_out, refs_out,
+                                workspace, _handle(stream))
+    out = Compacted((table, refs))
+    out.workspace = ws
+    return out

@@ -46,6 +46,21 @@ def test_too_few_pages_for_a_long_list_change_nothing(paged):
     assert int(table[half:, 0].max()) == P - 1
 
 
+def test_compact_says_what_it_found_without_a_workspace_of_the_callers(paged):
+    page, P = 16, 8
+    pool = torch.zeros(1, P, 1, page, 64, device="cuda")
+    refs, table = _ints([0, 0, 1, 0, 1, 0, 0, 1]), _ints([[4, 2, -1], [7, -1, -1]])
+    r = paged.compact(pool, pool.clone(), refs, table)
+    t, n = r
+    assert workspace_status(r.workspace) == OK
+    assert t.tolist() == [[0, 2, -1], [1, -1, -1]] and n.tolist() == [1, 1, 1, 0, 0, 0, 0, 0]
+    for wrong in (5, 8, 2 ** 31 - 1):          # nobody's page, and none of the pool's
+        table[1, 1] = wrong
+        r = paged.compact(pool, pool.clone(), refs, table)
+        assert workspace_status(r.workspace) == ERR_INDEX
+        assert r[0].tolist() == [[0, 2, -1], [1, wrong, -1]]
+
+
 # ------------------------------------------------------------------ streams
 def _calls(paged):
     """Each entry point as a call that takes a stream and gives its tensors."""
