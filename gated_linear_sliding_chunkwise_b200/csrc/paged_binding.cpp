@@ -96,6 +96,14 @@ void cuda_only(at::Device device) {
   if (!device.is_cuda()) refuse("the cache must be on a CUDA device");
 }
 
+// Without the interpreter's lock while it lives: an allocation may wait for the
+// device, and a launch for room in the stream's queue, which a callback of
+// another thread's may have to make.
+struct Unlocked {
+  PyThreadState *state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 // Runs f; what it throws becomes the Python exception.
 template <typename F> PyObject *guarded(F f) {
   HANDLE_TH_ERRORS
@@ -156,16 +164,21 @@ PyObject *attn(PyObject *, PyObject *const *a, Py_ssize_t n) {
     c.impl = number(a[17], "impl");
     cuda_only(device);
     const Place place(device, a[18]);
-    const Tensor o = out ? *out : at::empty({T, H, d}, q->options()),
-                 lse = want_lse ? at::empty({T, H}, q->options().dtype(at::kFloat)) : Tensor();
-    const Tensor ws = space(given, lizard_paged_attn_workspace_size(&c), device);
-    c.q = ptr(q); c.k = ptr(k); c.v = ptr(v); c.k_pages = ptr(kp); c.v_pages = ptr(vp);
-    c.table = ints(table); c.lens = ints(lens); c.cu_q = ints(cu); c.row = ints(row);
-    c.o = ptr(&o);
-    c.lse = lse.defined() ? static_cast<float *>(lse.data_ptr()) : nullptr;
-    c.workspace = ws.data_ptr();
-    c.workspace_bytes = ws.nbytes();
-    const lizard_status st = lizard_paged_attn(&c, place.handle());
+    Tensor o, lse, ws;
+    lizard_status st;
+    {
+      const Unlocked unlocked;
+      o = out ? *out : at::empty({T, H, d}, q->options());
+      if (want_lse) lse = at::empty({T, H}, q->options().dtype(at::kFloat));
+      ws = space(given, lizard_paged_attn_workspace_size(&c), device);
+      c.q = ptr(q); c.k = ptr(k); c.v = ptr(v); c.k_pages = ptr(kp); c.v_pages = ptr(vp);
+      c.table = ints(table); c.lens = ints(lens); c.cu_q = ints(cu); c.row = ints(row);
+      c.o = ptr(&o);
+      c.lse = lse.defined() ? static_cast<float *>(lse.data_ptr()) : nullptr;
+      c.workspace = ws.data_ptr();
+      c.workspace_bytes = ws.nbytes();
+      st = lizard_paged_attn(&c, place.handle());
+    }
     return Py_BuildValue("(iNNN)", (int)st, give(o), give(lse), give(ws));
   });
 }
@@ -213,24 +226,28 @@ PyObject *bookkeep(PyObject *, PyObject *const *a, Py_ssize_t n) {
     fits(refs_out, "refs_out", {P}, at::kInt, device);
     cuda_only(device);
     const Place place(device, a[13]);
-    Tensor to, ro;
-    if (op == 3) {
-      to = table_out ? *table_out : at::empty(table->sizes(), table->options());
-      ro = refs_out ? *refs_out : at::empty({P}, refs->options());
-      c.table_out = ints(&to);
-      c.refs_out = ints(&ro);
+    Tensor to, ro, ws;
+    lizard_status st;
+    {
+      const Unlocked unlocked;
+      if (op == 3) {
+        to = table_out ? *table_out : at::empty(table->sizes(), table->options());
+        ro = refs_out ? *refs_out : at::empty({P}, refs->options());
+        c.table_out = ints(&to);
+        c.refs_out = ints(&ro);
+      }
+      c.num_pages = P; c.rows = rows; c.max_pages = table->size(1); c.n = count;
+      ws = space(given, lizard_pages_workspace_size(&c), device);
+      c.refs = ints(refs); c.table = ints(table); c.lens = ints(lens);
+      c.row = ints(row); c.src = ints(src); c.grow = ints(grow);
+      c.workspace = ws.data_ptr();
+      c.workspace_bytes = ws.nbytes();
+      const auto call = op == 0   ? lizard_pages_reserve
+                        : op == 1 ? lizard_pages_free
+                        : op == 2 ? lizard_pages_fork
+                                  : lizard_pages_compact;
+      st = call(&c, place.handle());
     }
-    c.num_pages = P; c.rows = rows; c.max_pages = table->size(1); c.n = count;
-    const Tensor ws = space(given, lizard_pages_workspace_size(&c), device);
-    c.refs = ints(refs); c.table = ints(table); c.lens = ints(lens);
-    c.row = ints(row); c.src = ints(src); c.grow = ints(grow);
-    c.workspace = ws.data_ptr();
-    c.workspace_bytes = ws.nbytes();
-    const auto call = op == 0   ? lizard_pages_reserve
-                      : op == 1 ? lizard_pages_free
-                      : op == 2 ? lizard_pages_fork
-                                : lizard_pages_compact;
-    const lizard_status st = call(&c, place.handle());
     return Py_BuildValue("(iNNN)", (int)st, give(to), give(ro), give(ws));
   });
 }

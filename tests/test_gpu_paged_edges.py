@@ -2,6 +2,10 @@
 refusals found behind the list's checks, memory of other streams, rows that are
 computed again, results that must not depend on what ran before."""
 
+import sys
+import threading
+import time
+
 import pytest
 import torch
 
@@ -127,3 +131,39 @@ def test_a_call_on_another_stream_leaves_the_current_stream_alone(paged):
     s.synchronize()
     for x, y in zip(want[:2], got[:2]):
         assert torch.equal(x[:21], y[:21])     # the rows of the sequences
+
+
+def test_other_threads_run_while_a_call_launches(paged):
+    """The interpreter's lock is free during the launches.  With a switch
+    interval that never ends, another thread only gets its turn where a call
+    gives up the lock."""
+    turns, stop, ready = [0], threading.Event(), threading.Event()
+
+    def other():
+        ready.set()
+        while not stop.is_set():
+            turns[0] += 1
+            time.sleep(0)                      # gives up the lock at once
+
+    calls = _calls(paged)
+    for call in calls.values():
+        call(None)
+    torch.cuda.synchronize()
+    before, kept = sys.getswitchinterval(), []
+    thread = threading.Thread(target=other)
+    try:
+        sys.setswitchinterval(1000.0)
+        thread.start()
+        ready.wait()
+        for name in ("attn", "fork"):
+            seen = turns[0]
+            for _ in range(500):
+                kept.append(calls[name](None))
+                if turns[0] != seen:
+                    break
+            assert turns[0] != seen, name
+    finally:
+        sys.setswitchinterval(before)
+        stop.set()
+        thread.join()
+    torch.cuda.synchronize()
