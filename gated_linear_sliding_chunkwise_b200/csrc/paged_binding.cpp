@@ -161,6 +161,7 @@ PyObject *attn(PyObject *, PyObject *const *a, Py_ssize_t n) {
     c.softmax_scale = (float)PyFloat_AsDouble(a[15]);
     if (PyErr_Occurred()) throw python_error();
     const int want_lse = PyObject_IsTrue(a[16]);
+    if (want_lse < 0) throw python_error();
     c.impl = number(a[17], "impl");
     cuda_only(device);
     const Place place(device, a[18]);

@@ -153,3 +153,16 @@ def test_binding_refuses_tensors_that_do_not_fit(paged):
                  lambda: paged.free(refs, table, lens, i(0), page=16)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_a_truth_value_that_raises_is_the_callers_error(paged):
+    """want_lse's own exception comes through, and nothing is launched."""
+    class Undecided:
+        def __bool__(self):
+            raise ZeroDivisionError("undecided")
+
+    kp, x = torch.zeros(1, 4, 2, 16, 64), torch.zeros(2, 2, 64)
+    i = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ZeroDivisionError):
+        paged.attn(x, x, x, kp, kp, i[:, None].contiguous(), i, torch.zeros(3, dtype=torch.int32), max_q=1,
+                   want_lse=Undecided())
