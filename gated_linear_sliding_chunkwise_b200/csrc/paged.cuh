@@ -323,10 +323,11 @@ struct Partial {
 
 // ------------------------------------------------------------ exact row ---
 // One row of a piece, key by key with the mask applied to each: keys the row
-// does not see are not touched at all.  The tile kernels multiply masked
+// does not see are not touched at all.  The attention kernels multiply masked
 // values by a zero weight, which is not zero when such a value is infinite or
 // NaN; a row whose result is not finite is computed again here.  One warp;
-// lane l gets elements l * D / 32 ...
+// lane l gets elements l * D / 32 ...  It stops at a logit that is NaN: every
+// element is NaN from there on.
 template <typename T, int D>
 __device__ __noinline__ void exact_row(const PagedArgs &a, uint32_t *status, const Piece &p, int KT, int r, float *acc,
                                        float &m_out, float &l_out) {
@@ -340,7 +341,7 @@ __device__ __noinline__ void exact_row(const PagedArgs &a, uint32_t *status, con
   for (int e = 0; e < E; ++e) qv[e] = to_f32(q[e]), acc[e] = 0.f;
   float m = kNoKey, l = 0.f;
   const float c = a.scale * kLog2e;
-  for (int jt = p.j0; jt < p.j1; ++jt) {
+  for (int jt = p.j0; jt < p.j1 && !isnan(l); ++jt) {
     const int k0 = tile_index(p.t, jt) * KT;
     for (int j = k0; j < k0 + KT && j <= pos; ++j) {
       if (!sees(a, pos, j)) continue;
@@ -359,6 +360,7 @@ __device__ __noinline__ void exact_row(const PagedArgs &a, uint32_t *status, con
 #pragma unroll
       for (int e = 0; e < E; ++e) acc[e] = acc[e] * f + w * to_f32(v[e]);
       m = mn;
+      if (isnan(l)) break;
     }
   }
   m_out = m;
@@ -387,6 +389,42 @@ __device__ __noinline__ void exact_row_write(const PagedArgs &a, uint32_t *statu
   for (int e = 0; e < E; ++e) static_cast<T *>(a.o)[at * D + lane * E + e] = from_f32<T>(l == 0.f ? 0.f : acc[e] * inv);
   if (a.lse && lane == 0) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
+
+// The rows of a CTA's pieces whose results are not finite, as the kernel has
+// written them: computed again, by all warps of the CTA, when its pieces are
+// done.  That takes a warp 0.7 us per row and key (1500 tokens of a 16K prompt
+// with 16 heads: 0.19 s), so it is not done between pieces: there the CTA's
+// other warps are in waits that give up, and the pieces that follow may be
+// other users'.  A kernel that calls this leaves something that is not finite
+// in what it writes of every such row (an infinite sum of weights would make a
+// zero of it).
+template <typename T, int D, int KT>
+__device__ __noinline__ void exact_rows(const PagedArgs &a, uint32_t *status, const Work &work, int tok, int cls,
+                                        int slot_rows) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const Partial part{a.part_o[cls], reinterpret_cast<float2 *>(a.part_ml[cls])};
+  for (Cursor<KT> cur(a, work, tok, blockIdx.x); cur.valid(); cur.next()) {
+    const Piece &p = cur.p;
+    for (int r = warp; r < (p.i1 - p.i0) * a.g; r += warps) {
+      bool fine = true;
+      if (p.slot >= 0) {
+        const size_t at = (size_t)p.slot * slot_rows + r;
+        fine = isfinite(part.ml[at].y);
+#pragma unroll
+        for (int e = 0; e < E; ++e) fine = fine && isfinite(part.o[at * D + lane * E + e]);
+      } else {
+        const size_t at = (size_t)(p.q.t0 + p.i0 + token_of(a, r)) * a.H + p.h * a.g + head_of(a, r);
+#pragma unroll
+        for (int e = 0; e < E; ++e) fine = fine && isfinite(to_f32(static_cast<const T *>(a.o)[at * D + lane * E + e]));
+      }
+      if (__any_sync(0xffffffffu, !fine)) exact_row_write<T, D>(a, status, Piece(p), KT, r, part, slot_rows);
+    }
+  }
+}
+// 1 / sum of a row's weights: 0 for a row without keys, NaN for a sum that is
+// not finite (see exact_rows).
+LZ_DEV float inverse_sum(float l) { return !isfinite(l) ? NAN : l == 0.f ? 0.f : 1.f / l; }
 
 }  // namespace paged
 }  // namespace lz

@@ -34,11 +34,10 @@ template <int D> struct StreamSmem {
   unsigned char kv[stages<D>()][2][tile_bytes<D>()];   // 64-column regions of 64 rows, 128-byte swizzle
   unsigned char p[kStreamRows * 128];                  // weights, bf16 [row][key], 128-byte swizzle
   float m[kWarps][kStreamRows], l[kWarps][kStreamRows];
-  uint32_t odd[kWarps];
   long long prefix[kAlone + 1], warp_sums[kWarps + 1];   // the work, where there is no prep
   Seq seqs[kAlone];
   uint64_t full[stages<D>()], empty[stages<D>()];
-  uint32_t dead, found;
+  uint32_t dead, found, odd;                           // odd: some row is not finite
 };
 
 LZ_DEV uint32_t kv_offset(int row, int chunk) {   // 16-byte chunk of a row
@@ -272,7 +271,6 @@ __device__ void consume(const PagedArgs &a, const Work &work, StreamSmem<D> &sm,
       if ((lane & 3) == 0) sm.l[warp][r0 + 8 * x] = l[x];
     }
     tc::bar_sync(1, kWarps * 32);
-    unsigned odd = 0;                   // rows with something not finite in this warp's columns
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int r = r0 + 8 * x;
@@ -282,11 +280,8 @@ __device__ void consume(const PagedArgs &a, const Work &work, StreamSmem<D> &sm,
       bool fine = isfinite(ll);
 #pragma unroll
       for (int n = 0; n < NT; ++n) fine = fine && isfinite(o[n][2 * x]) && isfinite(o[n][2 * x + 1]);
-      const unsigned bad = __ballot_sync(0xffffffffu, r < rows && !fine);   // 4 lanes per row
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (bad >> (4 * i) & 15u) odd |= 1u << (8 * x + i);
       if (r >= rows) continue;
+      if (!fine) sm.odd = 1;
       if (p.slot >= 0) {
         const size_t at = (size_t)p.slot * kStreamRows + r;
 #pragma unroll
@@ -295,23 +290,13 @@ __device__ void consume(const PagedArgs &a, const Work &work, StreamSmem<D> &sm,
         if (warp == 0 && (lane & 3) == 0) part.ml[at] = make_float2(m[x], ll);
       } else {
         const size_t at = (size_t)(p.q.t0 + p.i0 + token_of(a, r)) * a.H + p.h * a.g + head_of(a, r);
-        const float inv = ll == 0.f ? 0.f : 1.f / ll;
+        const float inv = inverse_sum(ll);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
           *reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(a.o) + at * D + (warp * NT + n) * 8 + c0) =
               tc::pack_bf16(o[n][2 * x] * inv, o[n][2 * x + 1] * inv);
         if (a.lse && warp == 0 && (lane & 3) == 0) a.lse[at] = ll == 0.f ? -INFINITY : (m[x] + log2f(ll)) * kLn2;
       }
-    }
-    if (lane == 0) sm.odd[warp] = odd;
-    tc::bar_sync(1, kWarps * 32);       // also: the next piece writes the maxima and sums anew
-    unsigned rows_odd = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) rows_odd |= sm.odd[w];
-    if (rows_odd) {
-      // such a row is written again, by one warp, after every warp's columns of it
-      for (int r = warp; r < rows; r += kWarps)
-        if (rows_odd >> r & 1u) exact_row_write<__nv_bfloat16, D>(a, wait.status, Piece(p), kKeys, r, part, kStreamRows);
     }
   }
   if (threadIdx.x == 0) a.items[0][blockIdx.x] = item;
@@ -330,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       tc::mbar_init(&sm.full[i], 1);
       tc::mbar_init(&sm.empty[i], kWarps);
     }
-    sm.dead = sm.found = 0;
+    sm.dead = sm.found = sm.odd = 0;
     tc::fence_barrier_init();
   }
   __syncthreads();
@@ -340,6 +325,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   const Work work = ALONE ? find_work<D>(a, sm, least) : planned(a, 0);
   if (warp == kWarps) produce<D>(a, work, &kmap, &vmap, sm, wait);
   else consume<D, ALONE>(a, work, sm, wait);
+  __syncthreads();
+  if (sm.odd) exact_rows<__nv_bfloat16, D, kKeys>(a, wait.status, work, kStreamRows, 0, kStreamRows);
   if (ALONE) {
     __syncthreads();
     if (threadIdx.x == 0) a.found[blockIdx.x] = sm.found;

@@ -58,7 +58,7 @@ template <int D> struct TileSmem {
   unsigned char q[2][tile_bytes<D>()];
   unsigned char kv[slots<D>()][tile_bytes<D>()];  // K, V, K, V, ...
   uint64_t q_full, q_empty, kv_full[slots<D>()], kv_empty[slots<D>()], s_full[2], p_full[2][2], o_full[2];
-  uint32_t tmem, dead;
+  uint32_t tmem, dead, odd;                       // odd: some row is not finite
 };
 
 // One lane of a converged warp.  The issuing branches go by this and not by
@@ -315,7 +315,7 @@ __device__ void softmax(const PagedArgs &a, TileSmem<D> &sm, const Waits &wait, 
     const bool live = row < hf.rows;
     const size_t at = p.slot >= 0 ? (size_t)p.slot * kTileRows2 + r
                                   : (size_t)(p.q.t0 + p.i0 + token_of(a, r)) * a.H + p.h * a.g + head_of(a, r);
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const float inv = inverse_sum(l);
     bool fine = isfinite(l);
 #pragma unroll
     for (int c = 0; c < D; c += 32) {
@@ -340,9 +340,8 @@ __device__ void softmax(const PagedArgs &a, TileSmem<D> &sm, const Waits &wait, 
       if (p.slot >= 0) part.ml[at] = make_float2(m, l);
       else if (a.lse) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
     }
+    if (live && !fine) sm.odd = 1;
     tc::tc_fence_before();
-    for (unsigned odd = __ballot_sync(0xffffffffu, live && !fine); odd; odd &= odd - 1)
-      exact_row_write<__nv_bfloat16, D>(a, a.status, Piece(p), kKeys, x * tpt * a.g + wrow + __ffs(odd) - 1, part, kTileRows2);
   }
   if (threadIdx.x == 0) a.items[1][blockIdx.x] = item;
 }
@@ -368,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(&sm.p_full[i][1], 4);
       tc::mbar_init(&sm.o_full[i], 1);
     }
-    sm.dead = 0;
+    sm.dead = sm.odd = 0;
     tc::fence_barrier_init();
   }
   if (warp == 9) {
@@ -394,6 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::tc_fence_before();
   __syncthreads();
   if (warp == 9) tc::tmem_dealloc(tmem, kTmemCols);
+  if (sm.odd) exact_rows<__nv_bfloat16, D, kKeys>(a, a.status, planned(a, 1), 2 * tpt, 1, kTileRows2);
   if (beside) pdl_wait();
 }
 

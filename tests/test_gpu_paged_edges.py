@@ -167,3 +167,77 @@ def test_other_threads_run_while_a_call_launches(paged):
         stop.set()
         thread.join()
     torch.cuda.synchronize()
+
+
+# --------------------------------------------------- rows computed again
+def _long_case(seqs, *, H, Hkv, d, page, seed):
+    """A cache on the GPU with pages in order, too long for the model's builder."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    used = [pt.ceil_div(s, page) for _, s in seqs]
+    P = sum(used)
+
+    def normal(*shape):
+        return torch.randn(*shape, generator=gen, device="cuda").to(BF16)
+
+    table, at = torch.full((len(seqs), max(used)), -1, dtype=torch.int32), 0
+    for b, n in enumerate(used):
+        table[b, :n] = torch.arange(at, at + n)
+        at += n
+    T = sum(n for n, _ in seqs)
+    cu = torch.tensor([0] + [n for n, _ in seqs]).cumsum(0).to(torch.int32)
+    return dict(q=normal(T, H, d), k_pages=normal(1, P, Hkv, page, d), v_pages=normal(1, P, Hkv, page, d),
+                table=table.cuda(), lens=_ints([s for _, s in seqs]), cu=cu.cuda())
+
+
+def _check_tokens(name, c, r, tokens, seqs, d, skip=()):
+    """These tokens (sequence, index) against the model; columns `skip` are not finite."""
+    keep = [x for x in range(d) if x not in skip]
+    cu = c["cu"].tolist()
+    for b, i in tokens:
+        n, s = seqs[b]
+        t, p = cu[b] + i, s - n + i
+        ids = c["table"][b, : pt.ceil_div(s, c["k_pages"].shape[3])].long()
+        pools = [c[x][0, ids].cpu() for x in ("k_pages", "v_pages")]
+        pools[1][..., list(skip)] = 0
+        want = pt.attention(c["q"][t:t + 1].cpu(), *pools, torch.arange(len(ids))[None], torch.tensor([p + 1]),
+                            torch.tensor([0, 1]))
+        got = r["o"][t:t + 1].clone()
+        assert not torch.isfinite(got[..., list(skip)]).any()
+        got[..., list(skip)] = 0
+        assert torch.isfinite(got[..., keep]).all()
+        pt.check_attention(f"{name} {b} {i}", got, r["lse"][t:t + 1], want, d, BF16, True)
+
+
+@pytest.mark.parametrize("H,Hkv,d,page,seqs", [
+    (16, 4, 128, 64, [(1500, 16384), (77, 300), (40, 2000)]),              # chunks; one prompt is computed again
+    (16, 4, 64, 16, [(1, 16384)] * 6 + [(1, 700), (2, 5000)]),             # decoding
+], ids=["chunks", "decoding"])
+def test_an_infinite_value_of_a_long_sequence_leaves_the_others_alone(paged, H, Hkv, d, page, seqs):
+    """Every row of a long sequence sees an infinite value and is computed
+    again, key by key: no wait of the call's kernels gives up meanwhile, and
+    the other sequences of the batch are what they are without it."""
+    long = [b for b, (_, s) in enumerate(seqs) if s == 16384]
+    c = _long_case(seqs, H=H, Hkv=Hkv, d=d, page=page, seed=3)
+
+    def call():
+        r = paged.attn(c["q"], None, None, c["k_pages"], c["v_pages"], c["table"], c["lens"], c["cu"],
+                       max_q=max(n for n, _ in seqs), want_lse=True)
+        assert workspace_status(r["workspace"]) == OK
+        return r
+
+    plain = call()
+    for b in long:
+        c["v_pages"][0, int(c["table"][b, 0]), :, 3, 5] = torch.inf
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    start.record()
+    r = call()
+    end.record()
+    torch.cuda.synchronize()
+    print(f"PAGED rows computed again: {start.elapsed_time(end):.1f} ms")
+    cu = c["cu"].tolist()
+    for b in range(len(seqs)):
+        if b not in long:
+            assert torch.equal(plain["o"][cu[b]:cu[b + 1]], r["o"][cu[b]:cu[b + 1]])
+            assert torch.equal(plain["lse"][cu[b]:cu[b + 1]], r["lse"][cu[b]:cu[b + 1]])
+    _check_tokens("again", c, r, [(long[0], 0), (long[-1], seqs[long[-1]][0] - 1)], seqs, d, skip=(5,))
+    _check_tokens("beside", c, r, [(len(seqs) - 1, 0)], seqs, d)
