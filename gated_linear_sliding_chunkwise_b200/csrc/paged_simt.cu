@@ -250,6 +250,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(PagedArgs a, in
         }
       }
       const unsigned odd = __ballot_sync(0xffffffffu, r < rows && !fine);
+      if (odd) __syncwarp();                // such a row is written a second time, by other lanes
       for (int half = 0; half < 2; ++half)
         if (odd & (0xffffu << (16 * half)))
           exact_row_write<T, D>(a, a.status, Piece(p), kKeys, ((tid >> 5) * 2 + half) * 8 + i, part, kRows);

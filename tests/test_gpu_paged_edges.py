@@ -241,3 +241,25 @@ def test_an_infinite_value_of_a_long_sequence_leaves_the_others_alone(paged, H, 
             assert torch.equal(plain["lse"][cu[b]:cu[b + 1]], r["lse"][cu[b]:cu[b + 1]])
     _check_tokens("again", c, r, [(long[0], 0), (long[-1], seqs[long[-1]][0] - 1)], seqs, d, skip=(5,))
     _check_tokens("beside", c, r, [(len(seqs) - 1, 0)], seqs, d)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+def test_portable_rows_computed_again_keep_the_second_result(paged, dtype):
+    """A row is written once with what the tile's products gave and once more
+    key by key: what stays is the second, in every column, run after run."""
+    seqs, window = [(64, 64)] * 40, 9
+    c = pt.build([s for _, s in seqs], Hkv=1, d=64, page=16, dtype=dtype)
+    q, k, v, cu = _batch(seqs, H=1, Hkv=1, d=64, dtype=dtype, gap=0)
+    clean = {n: c[n].clone() for n in ("k_pages", "v_pages")}
+    for b in range(len(seqs)):                 # value 0: seen by tokens 0 .. 8, in the tile of all 64
+        c["v_pages"][0, int(c["table"][b, 0]), :, 0] = torch.inf
+    g = _cuda(c)
+    want = pt.attention(q, clean["k_pages"][0], clean["v_pages"][0], c["table"], c["lens"], cu, window=window)
+    sees = torch.arange(64).repeat(len(seqs)) < window
+    for _ in range(20):
+        r = paged.attn(q.cuda(), None, None, g["k_pages"], g["v_pages"], g["table"], g["lens"], cu.cuda(), max_q=64,
+                       window=window, want_lse=True, impl=IMPL_SIMT)
+        o = r["o"].cpu()
+        assert (o[sees] == torch.inf).all()
+        o[sees] = want[0][sees].to(dtype)
+        pt.check_attention("portable again", o, r["lse"], want, 64, dtype, rounded_weights=False)
