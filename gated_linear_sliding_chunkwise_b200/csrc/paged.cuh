@@ -35,6 +35,9 @@ constexpr float kNoKey = -FLT_MAX;   // running maximum before any key was seen
 // before it still runs; pdl_wait returns once that one has completed and its
 // writes are visible.
 LZ_DEV void pdl_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+// Orders what this thread has seen before it against all that it does after it,
+// over the whole GPU, TMA loads included.
+LZ_DEV void gpu_fence() { asm volatile("fence.acq_rel.gpu;\nfence.proxy.async;\n" ::: "memory"); }
 LZ_DEV void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 // Raises a kernel's shared-memory limit, once per device.
 struct SmemOnce {

@@ -319,7 +319,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     tc::fence_barrier_init();
   }
   __syncthreads();
-  if (!ALONE) pdl_wait();
+  if (!ALONE) {
+    pdl_wait();
+    gpu_fence();   // for the tile kernel, which starts on the triggers
+  }
   pdl_trigger();
   const Waits wait{&sm.dead, ALONE ? &sm.found : a.status};
   const Work work = ALONE ? find_work<D>(a, sm, least) : planned(a, 0);

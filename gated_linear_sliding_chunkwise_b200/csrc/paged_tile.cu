@@ -377,13 +377,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  // Beside the streaming kernel: each CTA of that one lets this one start only
-  // when the prep kernel has completed, so all that is read here is there.  Its
-  // CTAs take over SM by SM as that one's leave (a batch of 44 decoding and 4
-  // chunked sequences: 54.4 -> 48.2 us; SMs set apart for each of the two by
-  // their work: 58), and it waits for that one at its end, so that the join,
-  // which waits for this one, follows both.
-  if (!beside) pdl_wait();
+  // Beside the streaming kernel this one does not wait for it.  What it reads
+  // are the prep kernel's split and pages: each CTA of the streaming kernel lets
+  // this kernel start only after its own wait for the prep kernel, which has
+  // then completed with its writes visible, and a fence on either side of the
+  // start (there before the trigger, here) carries that over.  The start itself
+  // is what the two fences meet at: that a kernel's CTAs run after the triggers
+  // that let them start is how the launch works, not an order that the memory
+  // model names.  CTAs take over SM by SM as the streaming kernel's leave (a
+  // batch of 44 decoding and 4 chunked sequences: 54.4 -> 48.2 us; SMs set apart
+  // for each of the two by their work: 58), and they wait for that kernel at
+  // their end, so that the join, which waits for this one, follows both.
+  if (beside) gpu_fence();
+  else pdl_wait();
   pdl_trigger();
   const uint32_t tmem = sm.tmem;
   const Waits wait{&sm.dead, a.status};
