@@ -219,7 +219,7 @@ __device__ void softmax(const PagedArgs &a, TileSmem<D> &sm, const Waits &wait, 
     const Range range(a, p);
     const int base = p.q.s - p.q.n, first = base + hf.first, last = first + hf.tokens - 1;
     const int pos = row < hf.rows ? first + token_of(a, row) : -1;
-    const bool busy = wrow < hf.rows;         // some row of this warp is one of the item's
+    const bool live = row < hf.rows, busy = wrow < hf.rows;   // this row, some row of the warp is one of the item's
     // tiles within [clear0, clear1) need no mask here and no zeroed values
     const int clear0 = a.window > 0 ? last - a.window + 1 : 0, clear1 = base + p.i0 + 1;
     int k0 = tile_index(p.t, p.j0) * kKeys;
@@ -255,13 +255,17 @@ __device__ void softmax(const PagedArgs &a, TileSmem<D> &sm, const Waits &wait, 
       wait(&sm.s_full[x], ns++ & 1);
       tc::tc_fence_after();
       if (busy) {
-        if (__any_sync(0xffffffffu, m == kNoKey)) {     // a row has seen no key yet
+        // Only rows of the item are asked (the others' logits come from what
+        // shared memory held before, and what is moved for one row shows in the
+        // last bits of its neighbours).
+        // a row sees its first keys
+        if (__any_sync(0xffffffffu, live && m == kNoKey && hi >= 0 && (lo < kKeys - 1 || sk > 0))) {
           load(0);
           raise();
           load(C);
           raise();
         }
-        if (__any_sync(0xffffffffu, top > m + kSlack)) {
+        if (__any_sync(0xffffffffu, live && top > m + kSlack)) {
           const float mn = fmaxf(m, top), f = ex2(m - mn);     // f = 0 at the first key
           m = mn;
           l *= f;
@@ -312,7 +316,6 @@ __device__ void softmax(const PagedArgs &a, TileSmem<D> &sm, const Waits &wait, 
     if (!busy) continue;
     // out: 32 columns at a time, unnormalised sums for a split item
     const int r = x * tpt * a.g + row;
-    const bool live = row < hf.rows;
     const size_t at = p.slot >= 0 ? (size_t)p.slot * kTileRows2 + r
                                   : (size_t)(p.q.t0 + p.i0 + token_of(a, r)) * a.H + p.h * a.g + head_of(a, r);
     const float inv = inverse_sum(l);

@@ -263,3 +263,28 @@ def test_portable_rows_computed_again_keep_the_second_result(paged, dtype):
         assert (o[sees] == torch.inf).all()
         o[sees] = want[0][sees].to(dtype)
         pt.check_attention("portable again", o, r["lse"], want, 64, dtype, rounded_weights=False)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_bits_do_not_depend_on_the_call_before(paged, d):
+    """Seven heads to a kv head fill 126 of a tile's 128 rows: what another call
+    left in shared memory for the other two has no say in the results."""
+    page, many = 64, 48                         # nine tiles of keys to a CTA
+    c = _long_case([(36, 4000)] * many, H=7, Hkv=1, d=d, page=page, seed=8)
+    full = torch.randn(32 * many, 8, d, device="cuda").to(BF16)
+
+    def call(q, cu, window):
+        r = paged.attn(q, None, None, c["k_pages"], c["v_pages"], c["table"], c["lens"], cu, max_q=36, window=window,
+                       want_lse=True)
+        assert workspace_status(r["workspace"]) == OK
+        return r["o"], r["lse"]
+
+    cu8 = _ints(range(0, 32 * many + 1, 32))
+    for window in (0, 1500):
+        first = None
+        for scale in (0.0, 1.0, 30.0, 1000.0):
+            call((full * scale).to(BF16), cu8, 0)            # 128 rows in every tile
+            got = call(c["q"], c["cu"], window)
+            if first is None:
+                first = got
+            assert torch.equal(first[0], got[0]) and torch.equal(first[1], got[1]), (window, scale)
