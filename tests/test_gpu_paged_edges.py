@@ -288,3 +288,45 @@ def test_bits_do_not_depend_on_the_call_before(paged, d):
             if first is None:
                 first = got
             assert torch.equal(first[0], got[0]) and torch.equal(first[1], got[1]), (window, scale)
+
+
+# Queries of 4 and a key of x in every column have the logit 4 x sqrt(d), in
+# log2 units 46.2 x at d = 64 and 65.3 x at d = 128.
+@pytest.mark.parametrize("d,x", [(64, 2.25), (64, 3.5), (64, 8.0), (128, 1.625), (128, 2.5)],
+                         ids=["104", "162", "369", "106", "163"])
+@pytest.mark.parametrize("seqs,H,Hkv,jumps", [
+    # a piece of several tiles per CTA, whole items and split ones; keys from the first of the
+    # jump on stand out, by up to x, in the middle of the prompt, at a tile's ends, and where
+    # only the last of the new tokens see them
+    ([(130, 6000)], 8, 8, (300, 2431)), ([(130, 6000)], 8, 8, (2047, 2048)), ([(130, 6000)], 8, 8, (5950, 5999)),
+    ([(33, 1500)] * 12, 8, 2, (200, 1490)), ([(33, 1500)] * 24, 7, 1, (129, 1499))])
+def test_a_leap_of_the_maximum_within_a_tile(paged, d, x, seqs, H, Hkv, jumps):
+    """Logits that rise by more than 2^96, and by more than 2^128, over all
+    before them within one tile of keys, in weights formed with the maximum
+    from before: such rows are computed again; rows beside them that do not
+    see the leap are not touched by it."""
+    gen = torch.Generator().manual_seed(11)
+    page = 64
+    lens = [s for _, s in seqs]
+    c = pt.build(lens, Hkv=Hkv, d=d, page=page, dtype=BF16)
+    c["k_pages"] /= 64
+    q, _, _, cu = _batch(seqs, H=H, Hkv=Hkv, d=d, dtype=BF16, gap=0)
+    q.fill_(4.0)
+    for b in range(len(seqs)):
+        for j in jumps:
+            for i, y in enumerate((x, x - 1 / 64)):           # two weights that differ: neither is all of it
+                if j + i < lens[b]:
+                    c["k_pages"][0, int(c["table"][b, (j + i) // page]), :, (j + i) % page] = y
+    g = _cuda(c)
+    r = paged.attn(q.cuda(), None, None, g["k_pages"], g["v_pages"], g["table"], g["lens"], cu.cuda(),
+                   max_q=max(n for n, _ in seqs), want_lse=True)
+    assert workspace_status(r["workspace"]) == OK
+    some = [0, len(seqs) - 1] if len(seqs) > 1 else [0]       # the model is slow
+    for b in some:
+        a, z = int(cu[b]), int(cu[b + 1])
+        pick = sorted({*torch.randint(0, z - a, (6,), generator=gen).tolist(), 0, z - a - 1})
+        for i in pick:
+            p = lens[b] - (z - a) + i
+            want = pt.attention(q[a + i:a + i + 1], c["k_pages"][0], c["v_pages"][0], c["table"][b:b + 1],
+                                torch.tensor([p + 1]), torch.tensor([0, 1]))
+            pt.check_attention(f"leap {b} {i}", r["o"][a + i:a + i + 1], r["lse"][a + i:a + i + 1], want, d, BF16, True)
