@@ -3,14 +3,17 @@
     python -m gated_linear_sliding_chunkwise_b200.build [--force] [-v]
 
 Each ``csrc/*.cu`` is compiled to an object under ``_build/`` (skipped when
-newer than its sources), then linked into ``liblizard.so`` next to this file;
-``csrc/paged_binding.cpp`` becomes the extension module ``_paged_call.so``.
+newer than its sources), then linked into ``liblizard.so`` next to this file.
+That takes nvcc alone.  ``csrc/paged_binding.cpp`` then becomes the extension
+module ``_paged_call.so``, which takes a CUDA build of torch and g++; without
+them it is left out, and importing ``.paged`` says so.
 """
 
 from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
+import importlib.metadata
 import os
 import shutil
 import subprocess
@@ -85,26 +88,54 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     return LIB
 
 
-def build_binding(force: bool = False) -> str:
+def _torch_version():
+    """What the extension module is compiled against, without importing it; None without torch."""
+    try:
+        return f"torch {importlib.metadata.version('torch')}, python {sys.version_info[0]}.{sys.version_info[1]}\n"
+    except importlib.metadata.PackageNotFoundError:
+        return None
+
+
+def _without_binding(why: str):
+    sys.stderr.write(f"_paged_call.so, the paged cache's Python entry, is left out: {why}\n")
+
+
+def build_binding(force: bool = False):
     """The extension module of the paged cache: torch's headers, linked to
-    liblizard.so beside it."""
+    liblizard.so beside it.  Compiled again for another torch or Python: the
+    one that is there would not fit.  Returns its path, or None where it
+    cannot be compiled."""
     src = os.path.join(CSRC, "paged_binding.cpp")
-    if not force and not _stale(BINDING, [src, os.path.join(INCLUDE, "lizard.h")]):
+    stamp = os.path.join(BUILD, "paged_call.against")
+    against, before = _torch_version(), None
+    if os.path.exists(stamp):
+        with open(stamp) as f:
+            before = f.read()
+    if not force and against == before and not _stale(BINDING, [src, os.path.join(INCLUDE, "lizard.h")]):
         return BINDING
+    if os.path.exists(BINDING):              # not to be found by an import if it cannot be made anew
+        os.remove(BINDING)
+    gxx = shutil.which("g++")
+    if against is None or gxx is None:
+        return _without_binding("torch is not installed" if against is None else "there is no g++")
     import sysconfig
 
     import torch
     from torch.utils import cpp_extension as ext
+    if torch.version.cuda is None:
+        return _without_binding("torch is a build without CUDA")
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     include = [*ext.include_paths(), sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
-    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+    cmd = [gxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *(f"-I{d}" for d in include), src, "-o", BINDING, f"-L{HERE}", "-llizard", f"-L{libs}", "-ltorch_python",
            "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{libs}"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode:
         raise RuntimeError("building the binding failed:\n" + r.stdout + r.stderr)
+    with open(stamp, "w") as f:
+        f.write(against)
     return BINDING
 
 
