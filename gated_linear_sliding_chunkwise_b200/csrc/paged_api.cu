@@ -227,7 +227,7 @@ lizard_status run_pages(const lizard_pages_args *a, Op op, lizard_stream_t strea
   if (list && a->n == 0) return cuda_status(cudaMemsetAsync(ws, 0, sizeof(uint32_t), s));
   lz::PagesArgs p{};
   p.layers = a->layers; p.num_pages = a->num_pages; p.page = a->page; p.rows = a->rows;
-  p.max_pages = a->max_pages; p.n = a->n;
+  p.max_pages = a->max_pages; p.n = list ? a->n : 0;   // without a list, n has no say in the kernel's choice
   p.page_bytes = contents ? (size_t)a->Hkv * a->page * a->d * (a->dtype == LIZARD_BF16 ? 2 : 4) : 0;
   p.k_pages = a->k_pages; p.v_pages = a->v_pages;
   p.refs = a->refs; p.table = a->table; p.lens = a->lens;

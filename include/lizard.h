@@ -429,8 +429,8 @@ lizard_status lizard_prefill_cache(const lizard_cache_args *args, lizard_stream_
  *   refs              [num_pages] int32: how many rows hold a page; a page
  *                     with count 0 is free
  * Sizes: page in {16, 32, 64, 128}; d in {64, 128}; num_pages <= 2^22;
- * num_pages * Hkv * page < 2^31; rows * max_pages < 2^31 (addresses are
- * 64-bit throughout).
+ * num_pages * Hkv * page < 2^31; rows * max_pages < 2^31; max_pages * page
+ * <= 2^30 (addresses are 64-bit throughout).
  *
  * lizard_paged_attn: attention of new tokens over one layer's pages.  The
  * batch is ragged: sequence b's new tokens are rows cu_q[b] .. cu_q[b+1] - 1
@@ -514,12 +514,15 @@ lizard_status lizard_paged_attn(const lizard_paged_args *args, lizard_stream_t s
  *   keep their contents until they are handed out again).  row, src, grow
  *   and lens are not read.
  *
- * reserve, free and fork change everything or nothing: an index, length,
- * duplicate row or held page that is not allowed (LIZARD_ERR_INDEX) or too
- * few free pages (LIZARD_ERR_PAGES) is recorded in the workspace's status
- * word, which each call clears first, and nothing is changed.  compact
+ * reserve, free and fork change everything or nothing: an index, length or
+ * duplicate row that is not allowed, a held page outside the pool or with
+ * count 0 (free, fork; LIZARD_ERR_INDEX), or too few free pages
+ * (LIZARD_ERR_PAGES) is recorded in the workspace's status word, which each
+ * call clears first, and nothing is changed.  compact
  * leaves a table entry that is not a live page (and not negative) as it is
- * and records LIZARD_ERR_INDEX.  n = 0 is a no-op (compact does not read n).
+ * and records LIZARD_ERR_INDEX.  0 <= n <= rows in every call; n = 0 is a
+ * no-op, but not of compact, which has no list: there n only counts towards
+ * the workspace's size.
  * k_pages, v_pages, layers, Hkv, d and dtype are read by fork and compact
  * only.
  */

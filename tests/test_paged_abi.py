@@ -166,3 +166,14 @@ def test_a_truth_value_that_raises_is_the_callers_error(paged):
     with pytest.raises(ZeroDivisionError):
         paged.attn(x, x, x, kp, kp, i[:, None].contiguous(), i, torch.zeros(3, dtype=torch.int32), max_q=1,
                    want_lse=Undecided())
+
+
+def test_compact_takes_any_workspace_that_the_size_query_gives(paged, lz):
+    """compact has no list: n counts towards the workspace's size alone, and is checked like the others'."""
+    size = lz.lib().lizard_pages_workspace_size
+    bytes_of = [size(ctypes.byref(_pages(paged, lz, n=n))) for n in range(5)]
+    assert bytes_of == sorted(bytes_of) and bytes_of[0] > 0
+    for n in (-1, 5):
+        a = _pages(paged, lz, n=n)
+        assert size(ctypes.byref(a)) == 0
+        assert lz.lib().lizard_pages_compact(ctypes.byref(a), None) == lz.ERR_INVALID_ARG
