@@ -2,18 +2,24 @@
 // (decoding, a few tokens at a time), bf16.
 //
 // Bound by reading the cache: every key and value is used by at most 16 rows,
-// 32 operations per byte.  So the kernel keeps loads in flight: a producer
+// 16 operations per byte.  So the kernel keeps loads in flight: a producer
 // warp fetches tiles of 64 keys (32 KB of K and V at d = 128) by TMA into a
 // ring of 3 (d = 128) or 6 stages, two CTAs per SM, which is 192 KB under way
 // per SM where about 45 KB cover the latency at full bandwidth.  The products
 // run on warp-level mma.sync m16n8k16: a tcgen05 tile has 128 rows, of which
 // 112 or more would be empty here, and its round trip through TMEM would be
-// longer than the 16 + 16 products that each of the four consumer warps needs
+// longer than the 16 + 32 products that each of the four consumer warps needs
 // per tile.  A warp takes 16 of the tile's keys in the first product and D / 4
 // of the columns in the second, with the maxima and the weights handed over
 // in shared memory (two barriers of 128 threads a tile): no warp holds another
 // sum for the same output, so a piece ends without a join of the warps, which
 // took 4.6 us of a call with one token.
+//
+// The weights' product with the values is taken twice, with a weight's bf16
+// rounding and with what that leaves (also in bf16): the tensor pipe has the
+// time (20% busy with one product), and the output's error is that of its own
+// rounding, 1.66e-3 of it, where weights of one bf16 number gave 2.27e-3.  64
+// decoding sequences 353 -> 349 us, one token 11.9 us as before.
 //
 // A call that only has such sequences, at most kAlone of them, needs no kernel
 // before this one (ALONE): each CTA checks the batch and splits the work for
@@ -32,7 +38,7 @@ template <int D> constexpr int stages() { return D == 128 ? 3 : 6; }
 template <int D> constexpr uint32_t tile_bytes() { return kKeys * D * 2; }   // K or V
 template <int D> struct StreamSmem {
   unsigned char kv[stages<D>()][2][tile_bytes<D>()];   // 64-column regions of 64 rows, 128-byte swizzle
-  unsigned char p[kStreamRows * 128];                  // weights, bf16 [row][key], 128-byte swizzle
+  unsigned char p[2][kStreamRows * 128];               // weights in two bf16 parts [row][key], 128-byte swizzle
   float m[kWarps][kStreamRows], l[kWarps][kStreamRows];
   long long prefix[kAlone + 1], warp_sums[kWarps + 1];   // the work, where there is no prep
   Seq seqs[kAlone];
@@ -241,22 +247,30 @@ __device__ void consume(const PagedArgs &a, const Work &work, StreamSmem<D> &sm,
         for (int n = 0; n < 2; ++n) {
           const float w0 = ex2(s[n][2 * x] - m[x]), w1 = ex2(s[n][2 * x + 1] - m[x]);
           l[x] += w0 + w1;
-          // weights go to the second product in bf16 (half a step, 2^-8 of each); the sum keeps 32 bits
-          *reinterpret_cast<uint32_t *>(sm.p + tc::sw128_offset(r0 + 8 * x, warp * 16 + n * 8 + c0)) =
-              tc::pack_bf16(w0, w1);
+          // a weight goes to the second product as two bf16 numbers, which are off by at most 2^-16 of it
+          const uint32_t hi = tc::pack_bf16(w0, w1);
+          const float2 h = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&hi));
+          const uint32_t at = tc::sw128_offset(r0 + 8 * x, warp * 16 + n * 8 + c0);
+          *reinterpret_cast<uint32_t *>(sm.p[0] + at) = hi;
+          *reinterpret_cast<uint32_t *>(sm.p[1] + at) = tc::pack_bf16(w0 - h.x, w1 - h.y);
         }
       }
       tc::bar_sync(1, kWarps * 32);
 #pragma unroll
       for (int k = 0; k < kKeys / 16; ++k) {
-        uint32_t pf[4];
-        ldmatrix4(tc::smem_u32(sm.p) + tc::sw128_offset(lane & 15, k * 16 + (lane >> 4) * 8), pf);
+        uint32_t pf[2][4];
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          ldmatrix4(tc::smem_u32(sm.p[x]) + tc::sw128_offset(lane & 15, k * 16 + (lane >> 4) * 8), pf[x]);
 #pragma unroll
         for (int n = 0; n < NT; n += 2) {
           uint32_t b[4];
           ldmatrix4_t(va + kv_offset(k * 16 + (lane & 15), warp * NT + n + (lane >> 4)), b);
-          mma16816(o[n], pf, b[0], b[1]);
-          mma16816(o[n + 1], pf, b[2], b[3]);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            mma16816(o[n], pf[x], b[0], b[1]);
+            mma16816(o[n + 1], pf[x], b[2], b[3]);
+          }
         }
       }
       __syncwarp();

@@ -458,9 +458,10 @@ lizard_status lizard_prefill_cache(const lizard_cache_args *args, lizard_stream_
  *   max_q      upper bound of n_b (host value; selects the kernels)
  *   1 <= H / Hkv <= 64, H a multiple of Hkv; softmax_scale 0 means 1/sqrt(d)
  *   T = 0 or B = 0 is a no-op.
- * fp32: portable kernels.  bf16: tensor-core kernels (impl AUTO or TC), with
- * weights rounded to bf16 before their product with v, sums in fp32; or the
- * portable ones (impl SIMT).
+ * fp32: portable kernels.  bf16: tensor-core kernels (impl AUTO or TC), sums
+ * in fp32, or the portable ones (impl SIMT).  On the tensor cores the weights
+ * of a sequence with more than 16 rows (new tokens times H / Hkv) are rounded
+ * to bf16 before their product with v; those of fewer rows keep 16 bits.
  * Keys and values that no row may see have no effect, whatever they hold.
  * Found on the device, LIZARD_ERR_INDEX is recorded in the workspace's
  * status word (cleared by each call) for a sequence whose offsets, row,

@@ -330,3 +330,23 @@ def test_a_leap_of_the_maximum_within_a_tile(paged, d, x, seqs, H, Hkv, jumps):
             want = pt.attention(q[a + i:a + i + 1], c["k_pages"][0], c["v_pages"][0], c["table"][b:b + 1],
                                 torch.tensor([p + 1]), torch.tensor([0, 1]))
             pt.check_attention(f"leap {b} {i}", r["o"][a + i:a + i + 1], r["lse"][a + i:a + i + 1], want, d, BF16, True)
+
+
+# --------------------------------------------------------------- precision
+@pytest.mark.parametrize("H,Hkv,d,page", [(32, 8, 128, 64), (14, 2, 64, 16), (5, 5, 64, 128)])
+def test_decoding_keeps_its_weights_to_16_bits(paged, H, Hkv, d, page):
+    """At most 16 rows per key/value head: a weight goes to its product with v
+    as two bf16 numbers.  The first is off by half a step, 2^-8 of the weight,
+    the second by 2^-8 of that: 2^-16 of it stays, beside the bounds that
+    check_attention derives for logits, exp2, sums and the output's rounding."""
+    seqs = [(1, 1), (1, 70), (2, 517), (1, 2000), (2, 1300)]
+    c = pt.build([s for _, s in seqs], Hkv=Hkv, d=d, page=page, dtype=BF16)
+    q, _, _, cu = _batch(seqs, H=H, Hkv=Hkv, d=d, dtype=BF16, gap=0)
+    g = _cuda(c)
+    r = paged.attn(q.cuda(), None, None, g["k_pages"], g["v_pages"], g["table"], g["lens"], cu.cuda(), max_q=2)
+    o, _, A, mag = pt.attention(q, c["k_pages"][0], c["v_pages"][0], c["table"], c["lens"], cu)
+    weights = A * (2 * (d + 4) * 2.0 ** -22 * mag + 2.0 ** -20 + 2.0 ** -16).unsqueeze(-1)
+    half = torch.finfo(BF16).eps / 2
+    err = (r["o"].double().cpu() - o).abs()
+    assert (err <= weights * (1 + half) + half * o.abs() + 1e-30).all(), \
+        f"worst {float((err / (weights * (1 + half) + half * o.abs() + 1e-30)).max()):.2f} of the bound"
