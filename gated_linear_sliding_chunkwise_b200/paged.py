@@ -4,9 +4,10 @@ Argument marshalling only, like :mod:`.lizard`, but in a small extension module
 (``_paged_call``, ``csrc/paged_binding.cpp``): the smallest of these calls run
 for 10 us on the GPU.  The cache is the caller's tensors: k_pages, v_pages
 [layers, num_pages, Hkv, page, d], refs [num_pages], table [rows, max_pages]
-and lens [rows] (int32).  A serving loop calls ``reserve`` for the tokens to
-come, ``attn`` once per layer, ``fork`` and ``free`` as sequences branch and
-end, ``compact`` when the pool is to shrink.
+and lens [rows] (int32), contiguous and on 16-byte boundaries, as all tensors
+here.  A serving loop calls ``reserve`` for the tokens to come, ``attn`` once
+per layer, ``fork`` and ``free`` as sequences branch and end, ``compact`` when
+the pool is to shrink.
 
 Every call returns its workspace, or a result that includes it (``attn``,
 ``compact``); ``lizard.workspace_status(workspace)`` reads the call's device status.

@@ -177,3 +177,21 @@ def test_compact_takes_any_workspace_that_the_size_query_gives(paged, lz):
         a = _pages(paged, lz, n=n)
         assert size(ctypes.byref(a)) == 0
         assert lz.lib().lizard_pages_compact(ctypes.byref(a), None) == lz.ERR_INVALID_ARG
+
+
+def test_slices_off_a_16_byte_boundary_are_named(paged):
+    """The library wants pointers on 16-byte boundaries: the refusal says which tensor is not."""
+    kp, x = torch.zeros(1, 4, 2, 16, 64), torch.zeros(2, 2, 64)
+    i = torch.zeros(8, dtype=torch.int32)
+    good = dict(q=x, k=x, v=x, k_pages=kp, v_pages=kp, table=i[:8].view(2, 4), lens=i[:2], cu_q=i[:3], row=i[:2])
+    for name, bad in (("row", i[1:3]), ("lens", i[3:5]), ("cu_q", i[2:5]), ("table", i[1:7].view(2, 3)),
+                      ("q", torch.zeros(300)[1:257].view(2, 2, 64))):
+        with pytest.raises(ValueError, match=f"{name} must begin on a 16-byte boundary"):
+            paged.attn(**{**good, name: bad}, max_q=1)
+    refs, table = torch.zeros(5, dtype=torch.int32), i.view(2, 4)
+    with pytest.raises(ValueError, match="refs must begin"):
+        paged.free(refs[1:], table, i[:2], i[:1], page=16)
+    with pytest.raises(ValueError, match="row must begin"):
+        paged.free(refs, table, i[:2], i[1:2], page=16)
+    with pytest.raises(ValueError, match="CUDA"):            # an empty slice has no address
+        paged.free(refs, table, i[:2], i[1:1], page=16)
