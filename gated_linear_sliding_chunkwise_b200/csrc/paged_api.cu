@@ -13,6 +13,11 @@ constexpr size_t kHeader = 256;   // status word region at the workspace start
 size_t up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 bool ok_ptr(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 template <typename P> P *at(void *base, size_t off) { return reinterpret_cast<P *>(static_cast<char *>(base) + off); }
+// Whether [x, x + n) and [y, y + m) share a byte.
+bool overlap(const void *x, size_t n, const void *y, size_t m) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
+  return a < b + m && b < a + n;
+}
 lizard_status cuda_status(cudaError_t e) { return e == cudaSuccess ? LIZARD_OK : LIZARD_ERR_CUDA; }
 
 // Sizes of the pool and the table.
@@ -124,7 +129,10 @@ lizard_status lizard_paged_attn(const lizard_paged_args *a, lizard_stream_t stre
   const bool some = a->T > 0 && a->B > 0;
   if (some && (!a->q || !a->k_pages || !a->v_pages || !a->table || !a->lens || !a->cu_q || !a->o || a->max_q < 1))
     return LIZARD_ERR_INVALID_ARG;
-  if (some && a->o == a->q) return LIZARD_ERR_INVALID_ARG;   // o must not overlap q
+  const size_t row_bytes = (size_t)a->T * a->d * (a->dtype == LIZARD_BF16 ? 2 : 4);
+  for (const void *x : {a->q, a->k, a->v})
+    if (some && x && overlap(a->o, row_bytes * a->H, x, row_bytes * (x == a->q ? a->H : a->Hkv)))
+      return LIZARD_ERR_INVALID_ARG;
   const void *ptrs[] = {a->q, a->k, a->v, a->k_pages, a->v_pages, a->table, a->lens, a->cu_q, a->row,
                         a->o, a->lse, a->workspace};
   for (const void *p : ptrs)

@@ -195,3 +195,16 @@ def test_slices_off_a_16_byte_boundary_are_named(paged):
         paged.free(refs, table, i[:2], i[1:2], page=16)
     with pytest.raises(ValueError, match="CUDA"):            # an empty slice has no address
         paged.free(refs, table, i[:2], i[1:1], page=16)
+
+
+@pytest.mark.parametrize("name,heads", [("q", 4), ("k", 2), ("v", 2)])
+def test_an_output_over_any_part_of_the_inputs_is_refused(paged, lz, name, heads):
+    """o [7, 4, 64] bf16 against q [7, 4, 64], k and v [7, 2, 64], from either end."""
+    far = {n: (16 + i) * FAKE for i, n in enumerate(("q", "k", "v"))}
+    call, size = lz.lib().lizard_paged_attn, 7 * heads * 64 * 2
+    out = 7 * 4 * 64 * 2
+    for at, code in ((far[name] + size - 16, lz.ERR_INVALID_ARG), (far[name] - out + 16, lz.ERR_INVALID_ARG),
+                     (far[name], lz.ERR_INVALID_ARG), (far[name] + size, lz.ERR_WORKSPACE),
+                     (far[name] - out, lz.ERR_WORKSPACE)):
+        a = _attn(paged, lz, **far, o=at, workspace_bytes=100)      # the next check behind this one
+        assert call(ctypes.byref(a), None) == code
