@@ -66,8 +66,8 @@ cudaError_t pdl_launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
-// 2^x by the hardware unit alone (exp2f adds a rescaling for results below
-// 2^-126, which a weight may lose).
+// 2^x in one instruction; results below 2^-126 become zero, which a weight may
+// lose.
 LZ_DEV float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));

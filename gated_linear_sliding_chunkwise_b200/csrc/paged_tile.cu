@@ -35,8 +35,9 @@
 // What it took (8192 tokens of a 16K prompt, 32 heads on 8): 1.91 ms with a
 // maximum before the weights and the products issued by lane 0 (their
 // descriptors then go through vector registers, 120 cycles per product
-// instead of 64); 1.62 ms with an elected lane; 1.57 ms as it is now, 1.05
-// PFLOP/s.  Tried and left out: one S for both query tiles, so that QK_q(j+1)
+// instead of 64); 1.62 ms with an elected lane; 1.53 to 1.60 ms as it is now
+// (several B200s), 1.03 to 1.07 PFLOP/s, 63 to 65% of the measured bf16 rate.
+// Tried and left out: one S for both query tiles, so that QK_q(j+1)
 // need not wait for PV_q(j) (1.63 ms: all 128 logits of a row then have to be
 // in registers at once); sixteen softmax warps (1.55 ms, but a mixed batch 20%
 // slower); an issuing warp for each query tile (1.70 ms: the two tiles'
