@@ -130,9 +130,13 @@ lizard_status lizard_paged_attn(const lizard_paged_args *a, lizard_stream_t stre
   if (some && (!a->q || !a->k_pages || !a->v_pages || !a->table || !a->lens || !a->cu_q || !a->o || a->max_q < 1))
     return LIZARD_ERR_INVALID_ARG;
   const size_t row_bytes = (size_t)a->T * a->d * (a->dtype == LIZARD_BF16 ? 2 : 4);
-  for (const void *x : {a->q, a->k, a->v})
-    if (some && x && overlap(a->o, row_bytes * a->H, x, row_bytes * (x == a->q ? a->H : a->Hkv)))
+  for (const void *x : {a->q, a->k, a->v}) {
+    // a key or value is read before the output of its own token and head is
+    // written: with as many of them as query heads, o may be k or v itself
+    const bool itself = x != a->q && x == a->o && a->H == a->Hkv;
+    if (some && x && !itself && overlap(a->o, row_bytes * a->H, x, row_bytes * (x == a->q ? a->H : a->Hkv)))
       return LIZARD_ERR_INVALID_ARG;
+  }
   const void *ptrs[] = {a->q, a->k, a->v, a->k_pages, a->v_pages, a->table, a->lens, a->cu_q, a->row,
                         a->o, a->lse, a->workspace};
   for (const void *p : ptrs)

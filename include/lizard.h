@@ -452,7 +452,8 @@ lizard_status lizard_prefill_cache(const lizard_cache_args *args, lizard_stream_
  *              tokens may then be held by another row (lizard_pages_fork
  *              leaves it so)
  *   o          [T, H, d] dtype, written; rows from cu_q[B] on are left as they
- *              were.  It must not overlap q, k or v
+ *              were.  It must not overlap q, nor k or v (but may be one of
+ *              these two itself where H = Hkv)
  *   lse        [T, H] fp32 natural-log softmax normaliser, or NULL
  *   layer      which layer of the pool
  *   max_q      upper bound of n_b (host value; selects the kernels)

@@ -350,3 +350,22 @@ def test_decoding_keeps_its_weights_to_16_bits(paged, H, Hkv, d, page):
     err = (r["o"].double().cpu() - o).abs()
     assert (err <= weights * (1 + half) + half * o.abs() + 1e-30).all(), \
         f"worst {float((err / (weights * (1 + half) + half * o.abs() + 1e-30)).max()):.2f} of the bound"
+
+
+@pytest.mark.parametrize("seqs", [[(1, 70), (2, 1300), (1, 1)], [(90, 400), (1, 33), (300, 300)]], ids=["few", "chunks"])
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+def test_the_output_may_be_the_new_keys_or_values(paged, dtype, which, seqs):
+    """With as many key/value heads as query heads: the same bits as beside them."""
+    c = pt.build([s for _, s in seqs], Hkv=3, d=64, page=16, dtype=dtype)
+    q, k, v, cu = (x.cuda() for x in _batch(seqs, H=3, Hkv=3, d=64, dtype=dtype, gap=0))
+    outs = []
+    for beside in (True, False):
+        g = _cuda(c)
+        x = dict(k=k.clone(), v=v.clone())
+        r = paged.attn(q, x["k"], x["v"], g["k_pages"], g["v_pages"], g["table"], g["lens"], cu,
+                       max_q=max(n for n, _ in seqs), out=torch.empty_like(q) if beside else x[which])
+        assert workspace_status(r["workspace"]) == OK
+        outs.append([r["o"], g["k_pages"], g["v_pages"]])
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)

@@ -208,3 +208,5 @@ def test_an_output_over_any_part_of_the_inputs_is_refused(paged, lz, name, heads
                      (far[name] - out, lz.ERR_WORKSPACE)):
         a = _attn(paged, lz, **far, o=at, workspace_bytes=100)      # the next check behind this one
         assert call(ctypes.byref(a), None) == code
+    a = _attn(paged, lz, **far, H=2, o=far[name], workspace_bytes=100)   # as many query heads as the others
+    assert call(ctypes.byref(a), None) == (lz.ERR_INVALID_ARG if name == "q" else lz.ERR_WORKSPACE)
