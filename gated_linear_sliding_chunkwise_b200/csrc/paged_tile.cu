@@ -235,8 +235,12 @@ __device__ void softmax(const PagedArgs &a, TileSmem<D> &sm, const Waits &wait, 
     for (int j = 0; j < n; ++j, it += 2) {
       if (j > 0) k0 = p.j0 + j == p.t.nsink ? p.t.first * kKeys : k0 + kKeys;
       const bool clear = k0 >= clear0 && k0 + kKeys <= clear1;
-      if (!clear && !range.whole(k0, kKeys)) {
-        // values that no row sees may be anything: their weight is zero, so make them zero
+      if (x == 0 && !range.whole(k0, kKeys)) {
+        // Values that no row sees may be anything: their weight is zero, so make
+        // them zero.  The first query tile's warps do it for both: their weights
+        // are waited for before either product with V.  (The second's must not:
+        // they pass over pieces that have no rows for them, and a wait for a slot
+        // so far ahead of its loads would take an earlier load for this one.)
         const uint32_t v = it + 1;
         wait(&sm.kv_full[v % S], (v / S) & 1);
         for (int e = threadIdx.x & 127; e < kKeys * (D / 8); e += 128)

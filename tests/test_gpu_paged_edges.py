@@ -2,6 +2,8 @@
 refusals found behind the list's checks, memory of other streams, rows that are
 computed again, results that must not depend on what ran before."""
 
+import math
+import random
 import sys
 import threading
 import time
@@ -369,3 +371,45 @@ def test_the_output_may_be_the_new_keys_or_values(paged, dtype, which, seqs):
         outs.append([r["o"], g["k_pages"], g["v_pages"]])
     for a, b in zip(*outs):
         assert torch.equal(a, b)
+
+
+# ------------------------------------------- pieces of one and two query tiles
+@pytest.mark.parametrize("H,Hkv,d,page,window,sinks", [
+    (48, 1, 128, 32, 128, 0), (64, 1, 64, 64, 1, 0), (12, 2, 128, 128, 64, 3), (14, 2, 64, 16, 65, 1),
+    (7, 1, 128, 16, 17, 65), (24, 1, 64, 32, 0, 0)])
+def test_pieces_with_rows_for_one_query_tile_between_others(paged, H, Hkv, d, page, window, sinks):
+    """Hundreds of short sequences, so that a CTA has many pieces in a row: some
+    fill one query tile and leave the other's warps nothing, some have rows for
+    both, and nearly all end inside a tile of keys."""
+    gen = random.Random(H)
+    tokens = -(-128 // (H // Hkv))                           # of a query tile, rounded up
+    seqs = []
+    for _ in range(300):
+        n = gen.choice([1, 1, 1, tokens, tokens + 1, 2 * tokens, 4 * tokens]) if gen.random() < 0.5 else 1
+        n = min(n, 40)
+        seqs.append((n, n + gen.randint(0, 180)))
+    c = pt.build([s for _, s in seqs], Hkv=Hkv, d=d, page=page, dtype=BF16)
+    q, _, _, cu = _batch(seqs, H=H, Hkv=Hkv, d=d, dtype=BF16, gap=0)
+    g = _cuda(c)
+    want = [torch.cat(x) for x in zip(*(_plain(q, c, cu, b, s, window, sinks) for b, (_, s) in enumerate(seqs)))]
+    for _ in range(10):
+        r = paged.attn(q.cuda(), None, None, g["k_pages"], g["v_pages"], g["table"], g["lens"], cu.cuda(), max_q=40,
+                       window=window, sinks=sinks, want_lse=True)
+        assert workspace_status(r["workspace"]) == OK
+        pt.check_attention("pieces", r["o"], r["lse"], want, d, BF16, True)
+
+
+def _plain(q, c, cu, b, s, window, sinks):
+    """The model's attention of one sequence, all its tokens at once."""
+    a, z = int(cu[b]), int(cu[b + 1])
+    Hkv, page, d = c["k_pages"].shape[2], c["k_pages"].shape[3], q.shape[2]
+    k, v = (pt.gather(c[n][0], c["table"][b], s, page).repeat_interleave(q.shape[1] // Hkv, 0) for n in
+            ("k_pages", "v_pages"))                          # [H, s, d]
+    x = torch.einsum("nhd,hsd->nhs", q[a:z].double(), k) / math.sqrt(d)
+    mag = torch.einsum("nhd,hsd->nhs", q[a:z].double().abs(), k.abs()) / math.sqrt(d)
+    p, j = torch.arange(s - (z - a), s)[:, None], torch.arange(s)
+    see = (j <= p) & ((j > p - window) | (j < sinks) if window else True)
+    x = x.masked_fill(~see[:, None], -math.inf)
+    w = torch.softmax(x, -1)
+    return (torch.einsum("nhs,hsd->nhd", w, v), torch.logsumexp(x, -1), torch.einsum("nhs,hsd->nhd", w, v.abs()),
+            mag.masked_fill(~see[:, None], 0).amax(-1))
