@@ -117,8 +117,6 @@ def test_outputs_and_workspaces_belong_to_the_stream_of_the_call(paged, name, ha
     gone = _spans(out)
     del out                                    # dropped while the stream may be at work
     assert not _overlap(gone, _spans(blocks()))
-    with torch.cuda.stream(s):                 # they went back to the stream's own memory
-        assert _overlap(gone, _spans(blocks()))
     torch.cuda.synchronize()
 
 
